@@ -14,6 +14,10 @@ static inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t
 
 static inline bool good_scale(float s) { return std::isfinite(s) && s > 0.0f; }
 
+// A layer scale of the E2M1 cache: its products with block scales (2^-9 .. 448)
+// and their reciprocals stay normal binary32 numbers.
+static inline bool good_scale_e2m1(float s) { return good_scale(s) && s >= 0x1p-100f && s <= 0x1p100f; }
+
 static inline size_t round256(size_t x) { return (x + 255u) & ~size_t(255u); }
 
 WorkspaceLayout workspace_layout(int64_t rows_total, int32_t num_splits, int32_t head_dim)
@@ -127,6 +131,7 @@ struct AttnCall {
     void *stream;
     const void *k_new = nullptr;   // fused step: this step's new rows (fp16), appended in the launch
     const void *v_new = nullptr;
+    bool e2m1 = false;             // E2M1 pools (with e4m3 set, for the scales)
 };
 
 static int run_attention(const AttnCall &c, bool with_combine)
@@ -142,6 +147,11 @@ static int run_attention(const AttnCall &c, bool with_combine)
     if ((c.topk_idx == nullptr) != (c.topk_lens == nullptr)) return KVQ_ERR_INVALID_ARG;
     if (c.topk_idx && p.max_topk < 1) return KVQ_ERR_INVALID_ARG;
     if (c.e4m3 && (!good_scale(c.k_scale) || !good_scale(c.v_scale))) return KVQ_ERR_BAD_SCALE;
+    if (c.e2m1) {
+        if (!good_scale_e2m1(c.k_scale) || !good_scale_e2m1(c.v_scale)) return KVQ_ERR_BAD_SCALE;
+        // the E2M1 kernel has one decoder and one kernel for every shape
+        if (p.flags & ~int32_t(KVQ_ATTN_STRICT_ORDER)) return KVQ_ERR_UNSUPPORTED;
+    }
     // the FP8 scores exist on the tcgen05 kernel over E4M3 pools only
     if ((p.flags & KVQ_ATTN_FP8_QK) &&
         (!c.e4m3 || (p.flags & (KVQ_ATTN_BITCAST_DECODE | KVQ_ATTN_MMA_SYNC)) ||
@@ -210,7 +220,9 @@ static int run_attention(const AttnCall &c, bool with_combine)
 
     cudaStream_t stream = static_cast<cudaStream_t>(c.stream);
     bool merged = false;
-    if (launch_attention(c.e4m3, p.head_dim, a, stream, &merged) != cudaSuccess) return KVQ_ERR_CUDA;
+    if (c.e2m1) {
+        if (launch_attention_e2m1(p.head_dim, a, stream) != cudaSuccess) return KVQ_ERR_CUDA;
+    } else if (launch_attention(c.e4m3, p.head_dim, a, stream, &merged) != cudaSuccess) return KVQ_ERR_CUDA;
     if (with_combine && !merged &&
         launch_combine(a.ws_o, a.ws_m, a.ws_l, c.out, p.batch, p.q_len, p.num_q_heads, p.head_dim, S,
                        stream) != cudaSuccess)
@@ -253,7 +265,63 @@ static int check_prefill_params(const kvq_prefill_params *p)
     return KVQ_OK;
 }
 
-static int run_prefill(bool e4m3, const void *q, const void *k_cache, const void *v_cache,
+// shape, stride and pointer checks shared by the appends with rotary positions, then the launch
+static int run_append_rope(PoolKind pool, const void *q, const void *k_new, const void *v_new, const int32_t *positions,
+                           const float *table, const int32_t *slot_mapping, void *q_out, void *k_cache, void *v_cache,
+                           int64_t num_pages, float k_scale, float v_scale, const kvq_rope_params *p, int32_t *err_flag,
+                           void *stream)
+{
+    if (!p) return KVQ_ERR_INVALID_ARG;
+    if (p->num_tokens < 0 || p->num_q_heads < 0 || p->num_kv_heads < 1 || p->head_dim < 1 || p->rot_dim < 1 ||
+        p->max_positions < 1 || num_pages < 1 || (p->flags & ~int32_t(KVQ_ROPE_INTERLEAVED)))
+        return KVQ_ERR_INVALID_ARG;
+    if (p->head_dim % 16 != 0 || p->head_dim > 256) return KVQ_ERR_UNSUPPORTED;
+    if (pool == PoolKind::e2m1 && p->head_dim != 64 && p->head_dim != 128) return KVQ_ERR_UNSUPPORTED;
+    if (p->rot_dim > p->head_dim) return KVQ_ERR_INVALID_ARG;
+    if (p->rot_dim % 16 != 0 || p->num_q_heads > 65535 || p->num_kv_heads > 65535) return KVQ_ERR_UNSUPPORTED;
+    const int64_t q_row = int64_t(p->num_q_heads) * p->head_dim, kv_row = int64_t(p->num_kv_heads) * p->head_dim;
+    const int64_t qs = p->q_stride ? p->q_stride : q_row;
+    const int64_t ks = p->k_stride ? p->k_stride : kv_row, vs = p->v_stride ? p->v_stride : kv_row;
+    if (qs < q_row || ks < kv_row || vs < kv_row) return KVQ_ERR_INVALID_ARG;
+    if (pool == PoolKind::e4m3 && (!good_scale(k_scale) || !good_scale(v_scale))) return KVQ_ERR_BAD_SCALE;
+    if (pool == PoolKind::e2m1 && (!good_scale_e2m1(k_scale) || !good_scale_e2m1(v_scale))) return KVQ_ERR_BAD_SCALE;
+    if (p->num_tokens == 0) return KVQ_OK;
+    if (!k_new || !v_new || !positions || !table || !slot_mapping || !k_cache || !v_cache) return KVQ_ERR_INVALID_ARG;
+    if (p->num_q_heads > 0 && (!q || !q_out)) return KVQ_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(q_out) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(table) ||
+        !aligned16(k_cache) || !aligned16(v_cache) || qs % 8 || ks % 8 || vs % 8)
+        return KVQ_ERR_ALIGNMENT;
+    if (q_out == q && q && qs != q_row) return KVQ_ERR_INVALID_ARG;   // in place only where the layouts agree
+    RopeArgs a = {};
+    a.q = static_cast<const __half *>(q);
+    a.k = static_cast<const __half *>(k_new);
+    a.v = static_cast<const __half *>(v_new);
+    a.positions = positions;
+    a.slots = slot_mapping;
+    a.table = table;
+    a.q_out = static_cast<__half *>(q_out);
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.num_pages = num_pages;
+    a.q_stride = qs;
+    a.k_stride = ks;
+    a.v_stride = vs;
+    a.err_flag = err_flag;
+    a.num_tokens = p->num_tokens;
+    a.num_q_heads = p->num_q_heads;
+    a.num_kv_heads = p->num_kv_heads;
+    a.head_dim = p->head_dim;
+    a.rot_dim = p->rot_dim;
+    a.max_positions = p->max_positions;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.k_six = 6.0f * k_scale;
+    a.v_six = 6.0f * v_scale;
+    a.interleaved = (p->flags & KVQ_ROPE_INTERLEAVED) != 0;
+    return launch_append_rope(pool, true, a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+static int run_prefill(PoolKind pool, const void *q, const void *k_cache, const void *v_cache,
                        int64_t num_pages, const int32_t *block_tables, const int32_t *context_lens,
                        const int32_t *q_start, float k_scale, float v_scale, void *workspace,
                        size_t workspace_bytes, void *out, const kvq_prefill_params *p,
@@ -261,11 +329,13 @@ static int run_prefill(bool e4m3, const void *q, const void *k_cache, const void
 {
     const int st = check_prefill_params(p);
     if (st != KVQ_OK) return st;
+    const bool e4m3 = pool != PoolKind::fp16;   // pools with scales
     if (p->batch == 0) return KVQ_OK;
     if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !q_start || !out)
         return KVQ_ERR_INVALID_ARG;
     if (num_pages < 1) return KVQ_ERR_INVALID_ARG;
     if (e4m3 && (!good_scale(k_scale) || !good_scale(v_scale))) return KVQ_ERR_BAD_SCALE;
+    if (pool == PoolKind::e2m1 && (!good_scale_e2m1(k_scale) || !good_scale_e2m1(v_scale))) return KVQ_ERR_BAD_SCALE;
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
         !aligned16(workspace))
         return KVQ_ERR_ALIGNMENT;
@@ -296,7 +366,7 @@ static int run_prefill(bool e4m3, const void *q, const void *k_cache, const void
     a.total_q = p->total_q;
     a.qk_scale_log2 = float(sm * log2e * (e4m3 ? double(k_scale) : 1.0));
     a.out_scale = e4m3 ? v_scale : 1.0f;
-    return launch_prefill(e4m3, a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+    return launch_prefill(pool, a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
 }  // namespace kvq
@@ -496,7 +566,7 @@ int paged_prefill_attn_e4m3(const void *q, const uint8_t *k_cache, const uint8_t
                             size_t workspace_bytes, void *out, const kvq_prefill_params *p,
                             int32_t *err_flag, void *stream)
 {
-    return run_prefill(true, q, k_cache, v_cache, num_pages, block_tables, context_lens, q_start, k_scale,
+    return run_prefill(PoolKind::e4m3, q, k_cache, v_cache, num_pages, block_tables, context_lens, q_start, k_scale,
                        v_scale, workspace, workspace_bytes, out, p, err_flag, stream);
 }
 
@@ -505,8 +575,146 @@ int paged_prefill_attn_fp16(const void *q, const void *k_cache, const void *v_ca
                             void *workspace, size_t workspace_bytes, void *out, const kvq_prefill_params *p,
                             int32_t *err_flag, void *stream)
 {
-    return run_prefill(false, q, k_cache, v_cache, num_pages, block_tables, context_lens, q_start, 1.0f, 1.0f,
+    return run_prefill(PoolKind::fp16, q, k_cache, v_cache, num_pages, block_tables, context_lens, q_start, 1.0f, 1.0f,
                        workspace, workspace_bytes, out, p, err_flag, stream);
+}
+
+float kvq_scale_from_amax_e2m1(float amax)
+{
+    if (!std::isfinite(amax) || !(amax > 0.0f)) return 0.0f;
+    return amax / 2688.0f;
+}
+
+int kvq_rope_table(float *table, int32_t max_positions, int32_t rot_dim, double base, int32_t scaling, double factor,
+                   int32_t original_positions, double beta_fast, double beta_slow, double magnitude, void *stream)
+{
+    if (!table || max_positions < 1 || rot_dim < 1) return KVQ_ERR_INVALID_ARG;
+    if (scaling != KVQ_ROPE_NONE && scaling != KVQ_ROPE_LINEAR && scaling != KVQ_ROPE_YARN) return KVQ_ERR_INVALID_ARG;
+    if (rot_dim % 16 != 0) return KVQ_ERR_UNSUPPORTED;
+    if (!std::isfinite(base) || !(base > 1.0)) return KVQ_ERR_INVALID_ARG;
+    if (!std::isfinite(magnitude) || magnitude < 0.0) return KVQ_ERR_INVALID_ARG;
+    if (scaling != KVQ_ROPE_NONE && !(std::isfinite(factor) && factor >= 1.0)) return KVQ_ERR_INVALID_ARG;
+    double low = 0.0, high = 1.0;
+    if (scaling == KVQ_ROPE_YARN) {
+        if (original_positions < 1 || !std::isfinite(beta_fast) || !std::isfinite(beta_slow) || !(beta_slow > 0.0) ||
+            !(beta_fast > beta_slow))
+            return KVQ_ERR_INVALID_ARG;
+        // the pair whose angle turns `beta` times over the original positions
+        const double two_pi = 6.283185307179586;
+        auto pair_of = [&](double beta) {
+            return rot_dim * std::log(original_positions / (beta * two_pi)) / (2.0 * std::log(base));
+        };
+        low = std::fmax(std::floor(pair_of(beta_fast)), 0.0);
+        high = std::fmin(std::ceil(pair_of(beta_slow)), double(rot_dim - 1));
+        if (!(high > low)) high = low + 0.001;
+    }
+    if (magnitude == 0.0) magnitude = scaling == KVQ_ROPE_YARN ? 0.1 * std::log(factor) + 1.0 : 1.0;
+    return launch_rope_table(table, max_positions, rot_dim, base, scaling, factor, low, high, magnitude,
+                             static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? KVQ_OK
+               : KVQ_ERR_CUDA;
+}
+
+int kv_append_rope_e4m3(const void *q, const void *k_new, const void *v_new, const int32_t *positions, const float *table,
+                        const int32_t *slot_mapping, void *q_out, uint8_t *k_cache, uint8_t *v_cache, int64_t num_pages,
+                        float k_scale, float v_scale, const kvq_rope_params *p, int32_t *err_flag, void *stream)
+{
+    return run_append_rope(PoolKind::e4m3, q, k_new, v_new, positions, table, slot_mapping, q_out, k_cache, v_cache,
+                           num_pages, k_scale, v_scale, p, err_flag, stream);
+}
+
+int kv_append_rope_fp16(const void *q, const void *k_new, const void *v_new, const int32_t *positions, const float *table,
+                        const int32_t *slot_mapping, void *q_out, void *k_cache, void *v_cache, int64_t num_pages,
+                        const kvq_rope_params *p, int32_t *err_flag, void *stream)
+{
+    return run_append_rope(PoolKind::fp16, q, k_new, v_new, positions, table, slot_mapping, q_out, k_cache, v_cache,
+                           num_pages, 1.0f, 1.0f, p, err_flag, stream);
+}
+
+int kv_append_rope_e2m1(const void *q, const void *k_new, const void *v_new, const int32_t *positions, const float *table,
+                        const int32_t *slot_mapping, void *q_out, uint8_t *k_cache, uint8_t *v_cache, int64_t num_pages,
+                        float k_scale, float v_scale, const kvq_rope_params *p, int32_t *err_flag, void *stream)
+{
+    return run_append_rope(PoolKind::e2m1, q, k_new, v_new, positions, table, slot_mapping, q_out, k_cache, v_cache,
+                           num_pages, k_scale, v_scale, p, err_flag, stream);
+}
+
+int kv_append_e2m1(const void *k_new, const void *v_new, const int32_t *slot_mapping, int32_t num_tokens,
+                   int32_t num_kv_heads, int32_t head_dim, uint8_t *k_cache, uint8_t *v_cache, int64_t num_pages,
+                   float k_scale, float v_scale, int32_t *err_flag, void *stream)
+{
+    if (num_tokens < 0 || num_kv_heads < 1 || num_pages < 1) return KVQ_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128) return KVQ_ERR_UNSUPPORTED;
+    if (num_kv_heads > 65535) return KVQ_ERR_UNSUPPORTED;
+    if (!good_scale_e2m1(k_scale) || !good_scale_e2m1(v_scale)) return KVQ_ERR_BAD_SCALE;
+    if (num_tokens == 0) return KVQ_OK;
+    if (!k_new || !v_new || !slot_mapping || !k_cache || !v_cache) return KVQ_ERR_INVALID_ARG;
+    if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_cache) || !aligned16(v_cache)) return KVQ_ERR_ALIGNMENT;
+    RopeArgs a = {};
+    a.k = static_cast<const __half *>(k_new);
+    a.v = static_cast<const __half *>(v_new);
+    a.slots = slot_mapping;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.num_pages = num_pages;
+    a.k_stride = a.v_stride = int64_t(num_kv_heads) * head_dim;
+    a.err_flag = err_flag;
+    a.num_tokens = num_tokens;
+    a.num_kv_heads = num_kv_heads;
+    a.head_dim = head_dim;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.k_six = 6.0f * k_scale;
+    a.v_six = 6.0f * v_scale;
+    return launch_append_rope(PoolKind::e2m1, false, a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK
+                                                                                                          : KVQ_ERR_CUDA;
+}
+
+int kv_gather_e2m1(const uint8_t *k_cache, const uint8_t *v_cache, int64_t num_pages, const int32_t *slots,
+                   int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim, float k_scale, float v_scale, void *k_out,
+                   void *v_out, int32_t *err_flag, void *stream)
+{
+    if (num_tokens < 0 || num_kv_heads < 1 || num_pages < 1) return KVQ_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128) return KVQ_ERR_UNSUPPORTED;
+    if (!good_scale_e2m1(k_scale) || !good_scale_e2m1(v_scale)) return KVQ_ERR_BAD_SCALE;
+    if (num_tokens == 0) return KVQ_OK;
+    if (!k_cache || !v_cache || !slots || !k_out || !v_out) return KVQ_ERR_INVALID_ARG;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_out) || !aligned16(v_out)) return KVQ_ERR_ALIGNMENT;
+    return launch_gather_e2m1(k_cache, v_cache, num_pages, slots, num_tokens, num_kv_heads, head_dim, k_scale, v_scale,
+                              k_out, v_out, err_flag, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? KVQ_OK
+               : KVQ_ERR_CUDA;
+}
+
+int paged_decode_attn_e2m1(const void *q, const uint8_t *k_cache, const uint8_t *v_cache, int64_t num_pages,
+                           const int32_t *block_tables, const int32_t *context_lens, float k_scale, float v_scale,
+                           const int32_t *topk_idx, const int32_t *topk_lens, float *workspace, size_t workspace_bytes,
+                           void *out, const kvq_attn_params *p, int32_t *err_flag, void *stream)
+{
+    AttnCall c{true, q, k_cache, v_cache, num_pages, block_tables, context_lens, k_scale, v_scale, topk_idx, topk_lens,
+               workspace, workspace_bytes, out, p, err_flag, stream};
+    c.e2m1 = true;
+    return run_attention(c, true);
+}
+
+int paged_decode_attn_e2m1_partial(const void *q, const uint8_t *k_cache, const uint8_t *v_cache, int64_t num_pages,
+                                   const int32_t *block_tables, const int32_t *context_lens, float k_scale, float v_scale,
+                                   const int32_t *topk_idx, const int32_t *topk_lens, float *workspace,
+                                   size_t workspace_bytes, const kvq_attn_params *p, int32_t *err_flag, void *stream)
+{
+    AttnCall c{true, q, k_cache, v_cache, num_pages, block_tables, context_lens, k_scale, v_scale, topk_idx, topk_lens,
+               workspace, workspace_bytes, nullptr, p, err_flag, stream};
+    c.e2m1 = true;
+    return run_attention(c, false);
+}
+
+int paged_prefill_attn_e2m1(const void *q, const uint8_t *k_cache, const uint8_t *v_cache, int64_t num_pages,
+                            const int32_t *block_tables, const int32_t *context_lens, const int32_t *q_start,
+                            float k_scale, float v_scale, void *workspace, size_t workspace_bytes, void *out,
+                            const kvq_prefill_params *p, int32_t *err_flag, void *stream)
+{
+    return run_prefill(PoolKind::e2m1, q, k_cache, v_cache, num_pages, block_tables, context_lens, q_start, k_scale,
+                       v_scale, workspace, workspace_bytes, out, p, err_flag, stream);
 }
 
 }  // extern "C"

@@ -3,11 +3,31 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "kvq.h"
 
 namespace kvq {
+
+// what a K/V pool holds
+enum class PoolKind { fp16, e4m3, e2m1 };
+
+// Arguments of an append with rotary positions (device pointers); the plain
+// append to the E2M1 cache uses those of K and V.
+struct RopeArgs {
+    const __half *q, *k, *v;     // [T][heads][head_dim], token strides below (elements)
+    const int32_t *positions, *slots;   // [T]
+    const float *table;          // [max_positions][rot_dim]: cos, then sin
+    __half *q_out;               // [T][Hq][head_dim]
+    void *k_cache, *v_cache;
+    int64_t num_pages, q_stride, k_stride, v_stride;
+    int32_t *err_flag;
+    int32_t num_tokens, num_q_heads, num_kv_heads, head_dim, rot_dim, max_positions;
+    float k_scale, v_scale, k_six, v_six;   // *_six: fl(6 * scale), E2M1
+    bool interleaved;
+    int32_t lanes, heads_per_warp, chunks;  // set by the launcher
+};
 
 // Arguments of one split-K attention launch (device pointers).
 struct AttnArgs {
@@ -67,7 +87,7 @@ struct PrefillArgs {
 size_t prefill_tiles_bytes(int32_t batch, int32_t num_kv_heads, int32_t max_tiles);
 size_t prefill_mask_offset(int32_t batch, int32_t num_kv_heads, int32_t max_tiles);
 int32_t prefill_max_tiles(int32_t max_pages);
-cudaError_t launch_prefill(bool e4m3, const PrefillArgs &a, cudaStream_t stream);
+cudaError_t launch_prefill(PoolKind pool, const PrefillArgs &a, cudaStream_t stream);
 
 struct WorkspaceLayout {
     size_t o_off, m_off, l_off, total;
@@ -94,6 +114,16 @@ cudaError_t launch_attention_tc(bool e4m3, const AttnArgs &a, cudaStream_t strea
 cudaError_t launch_attention_step(bool e4m3, int head_dim, const AttnArgs &a, cudaStream_t stream);
 cudaError_t launch_append_step(bool e4m3, int head_dim, const AttnArgs &a, cudaStream_t stream);
 bool tc_supported(int head_dim, int rows);
+// split-K attention over E2M1 pools: partials only (kvq_attn_e2m1.cu)
+cudaError_t launch_attention_e2m1(int head_dim, const AttnArgs &a, cudaStream_t stream);
+// append with rotary positions, or (rotate false) the plain append to E2M1 pools; the E2M1
+// read-back; the rotation table (kvq_rope.cu)
+cudaError_t launch_append_rope(PoolKind pool, bool rotate, RopeArgs a, cudaStream_t stream);
+cudaError_t launch_gather_e2m1(const void *k_cache, const void *v_cache, int64_t num_pages, const int32_t *slots,
+                               int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim, float k_scale, float v_scale,
+                               void *k_out, void *v_out, int32_t *err_flag, cudaStream_t stream);
+cudaError_t launch_rope_table(float *table, int32_t max_positions, int32_t rot_dim, double base, int32_t kind, double factor,
+                              double low, double high, double magnitude, cudaStream_t stream);
 cudaError_t launch_combine(const float *ws_o, const float *ws_m, const float *ws_l, void *out,
                            int32_t batch, int32_t q_len, int32_t num_q_heads, int32_t head_dim,
                            int32_t num_splits, cudaStream_t stream);

@@ -51,6 +51,7 @@
 #include <cuda_runtime.h>
 
 #include "kvq_device.cuh"
+#include "kvq_e2m1.cuh"
 #include "kvq_internal.h"
 #include "kvq_tcgen05.cuh"
 
@@ -107,9 +108,10 @@ __device__ __forceinline__ bool seq_ok(const PrefillArgs &a, int q0, int q1, int
 // ---------------------------------------------------------------------------
 // 1. pages -> fp16 tiles
 
-template <bool E4M3>
+template <PoolKind POOL>
 __global__ void __launch_bounds__(256) kv_tile_kernel(const PrefillArgs a)
 {
+    constexpr bool E4M3 = POOL == PoolKind::e4m3, E2M1 = POOL == PoolKind::e2m1;
     // four blocks per tile: K or V (kv), keys 0-63 or 64-127 (kh)
     const int j = blockIdx.x >> 2, kv = (blockIdx.x >> 1) & 1, kh = blockIdx.x & 1;
     const int g = blockIdx.y, b = blockIdx.z;
@@ -145,12 +147,18 @@ __global__ void __launch_bounds__(256) kv_tile_kernel(const PrefillArgs a)
         in_ctx[u] = pos < L;
         page[u] = in_ctx[u] ? __ldg(bt_row + (pos >> 2)) : -1;
     }
-    using Raw = typename std::conditional<E4M3, uint2, uint4>::type;
+    using Raw = typename std::conditional<E4M3, uint2, typename std::conditional<E2M1, uint32_t, uint4>::type>::type;
     Raw x[KI];
+    uint32_t block_scale[KI];
 #pragma unroll
     for (int u = 0; u < KI; ++u) {
         const int pos = j * kPfTile + key[u];
-        if (in_ctx[u] && page[u] >= 0 && page[u] < a.num_pages)
+        if (!(in_ctx[u] && page[u] >= 0 && page[u] < a.num_pages)) continue;
+        if constexpr (E2M1) {
+            const uint8_t *pg = pool + ((int64_t)page[u] * a.num_kv_heads + g) * e2m1_page_bytes(kPfD);
+            x[u] = __ldg(reinterpret_cast<const uint32_t *>(pg + (pos & 3) * (kPfD / 2)) + c8[u]);
+            block_scale[u] = __ldg(pg + e2m1_scale_off(kPfD) + (c8[u] / 2) * 4 + (pos & 3));
+        } else
             x[u] = __ldg(reinterpret_cast<const Raw *>(
                 pool + ((((int64_t)page[u] * a.num_kv_heads + g) * 4 + (pos & 3)) * kPfD + c8[u] * 8) * kElem));
     }
@@ -160,7 +168,11 @@ __global__ void __launch_bounds__(256) kv_tile_kernel(const PrefillArgs a)
         if (in_ctx[u] && page[u] >= 0 && page[u] < a.num_pages) {
             if constexpr (E4M3)
                 v = make_uint4(cvt_lo(x[u].x), cvt_hi(x[u].x), cvt_lo(x[u].y), cvt_hi(x[u].y));
-            else
+            else if constexpr (E2M1) {   // code times block scale: exact in fp16
+                const uint32_t bs = cvt_lo(block_scale[u] * 0x0101u);
+                v = make_uint4(hmul2(e2m1_pair<0>(x[u]), bs), hmul2(e2m1_pair<1>(x[u]), bs),
+                               hmul2(e2m1_pair<2>(x[u]), bs), hmul2(e2m1_pair<3>(x[u]), bs));
+            } else
                 v = x[u];
         } else if (in_ctx[u] && kv == 0 && c8[u] == 0) {
             report(a.err_flag, KVQ_DEV_BAD_PAGE);   // the row stays zero and its key is masked
@@ -604,9 +616,10 @@ size_t prefill_tiles_bytes(int32_t batch, int32_t num_kv_heads, int32_t max_tile
 
 int32_t prefill_max_tiles(int32_t max_pages) { return (int32_t)(((int64_t)max_pages * 4 + kPfTile - 1) / kPfTile); }
 
-template <bool E4M3>
+template <PoolKind POOL>
 static cudaError_t launch_prefill_t(const PrefillArgs &a, cudaStream_t stream)
 {
+    constexpr bool E4M3 = POOL != PoolKind::fp16;   // the attention reads the same tiles for every pool type
     static uint64_t configured = 0;   // one bit per device ordinal
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -617,7 +630,7 @@ static cudaError_t launch_prefill_t(const PrefillArgs &a, cudaStream_t stream)
         if (e != cudaSuccess) return e;
         __atomic_fetch_or(&configured, 1ull << dev, __ATOMIC_ACQ_REL);
     }
-    e = launch_pdl(kv_tile_kernel<E4M3>, dim3(4 * a.max_tiles, a.num_kv_heads, a.batch), dim3(256), 0, stream, a);
+    e = launch_pdl(kv_tile_kernel<POOL>, dim3(4 * a.max_tiles, a.num_kv_heads, a.batch), dim3(256), 0, stream, a);
     if (e != cudaSuccess) return e;
     // one CTA per SM, each taking its work items in turn
     const int64_t items = (int64_t)((a.max_q_len + 2 * kPfTile - 1) / (2 * kPfTile)) * a.batch * a.num_q_heads;
@@ -626,10 +639,11 @@ static cudaError_t launch_prefill_t(const PrefillArgs &a, cudaStream_t stream)
     return launch_pdl(prefill_attn_kernel<E4M3>, grid, dim3(kPfThreads), kPfSmemBytes, stream, a);
 }
 
-cudaError_t launch_prefill(bool e4m3, const PrefillArgs &a, cudaStream_t stream)
+cudaError_t launch_prefill(PoolKind pool, const PrefillArgs &a, cudaStream_t stream)
 {
     if (a.batch == 0) return cudaSuccess;
-    return e4m3 ? launch_prefill_t<true>(a, stream) : launch_prefill_t<false>(a, stream);
+    if (pool == PoolKind::e2m1) return launch_prefill_t<PoolKind::e2m1>(a, stream);
+    return pool == PoolKind::e4m3 ? launch_prefill_t<PoolKind::e4m3>(a, stream) : launch_prefill_t<PoolKind::fp16>(a, stream);
 }
 
 }  // namespace kvq

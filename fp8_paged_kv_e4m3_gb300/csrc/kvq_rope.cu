@@ -1,0 +1,304 @@
+// kvq_rope.cu -- rotary positions applied on the way into the paged cache,
+// the plain append to the E2M1 cache, and the E2M1 cache's read-back.
+//
+// Rotation of the channel pair (x1, x2) of a token at position p, with
+// c = cos and s = sin of its angle p * f_j (times the table's factor):
+//     y1 = fl(fl(x1 c) - fl(x2 s)),   y2 = fl(fl(x2 c) + fl(x1 s))
+// in binary32.  The queries are rounded to fp16 once; the keys go from these
+// binary32 values straight to the pool's type, one rounding (through fp16
+// first, a key would be rounded twice).
+#include <cstdint>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "kvq_device.cuh"
+#include "kvq_e2m1.cuh"
+#include "kvq_internal.h"
+
+namespace kvq {
+
+namespace {
+
+constexpr unsigned kAll = 0xFFFFFFFFu;
+constexpr int kRopeThreads = 256;
+
+// eight fp16 <-> eight fp32
+__device__ __forceinline__ void unpack8(uint4 h, float (&x)[8])
+{
+    const uint32_t w[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&y)[8])
+{
+    return make_uint4(pack_half2(y[0], y[1]), pack_half2(y[2], y[3]), pack_half2(y[4], y[5]), pack_half2(y[6], y[7]));
+}
+
+// eight fp32 -> eight E4M3 bytes, each divided by the scale in binary32
+__device__ __forceinline__ uint2 quantize8(const float (&y)[8], float scale)
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(y[2 * i], scale), __fdiv_rn(y[2 * i + 1], scale)),
+                                        __NV_SATFINITE, __NV_E4M3);
+    return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// Append with the rotation on the way.  A token's heads are its queries (Hq),
+// keys (Hkv) and values (Hkv); a lane owns 8 consecutive channels of a head, a
+// warp holds whole heads (D / 8 lanes each), so that a pair's other half comes
+// from a lane of the warp (half layout: half / 8 lanes away; interleaved: the
+// lane itself) and rotating the queries in place is safe: every load precedes
+// the shuffles, every store follows them.  A warp takes kIter groups of heads
+// of one token, loading all of them before the table entries, which it reads
+// once for all.  ROTATE = false is the plain append (keys and values only).
+constexpr int kIter = 4;
+
+template <PoolKind POOL, bool ROTATE>
+__global__ void __launch_bounds__(kRopeThreads) append_rope_kernel(const RopeArgs a)
+{
+    grid_dependency_wait();   // the projections and indices may come from the previous kernel
+    launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t w = ((int64_t)blockIdx.x * kRopeThreads + threadIdx.x) >> 5;
+    const int64_t token = w / a.chunks;
+    if (token >= a.num_tokens) return;
+    const int chunk = (int)(w - token * a.chunks);
+    const int sub = lane / a.lanes;                    // which of the warp's heads this lane belongs to
+    const int vec = lane - sub * a.lanes;
+    const bool live = sub < a.heads_per_warp;          // lanes past the last whole head idle
+    const int ch = vec * 8;
+    const int heads = a.num_q_heads + 2 * a.num_kv_heads;
+    const int32_t slot = __ldg(a.slots + token);
+    const int pos = ROTATE ? __ldg(a.positions + token) : 0;
+    if (ROTATE && (pos < 0 || pos >= a.max_positions)) {   // the same on every lane
+        if (chunk == 0 && lane == 0) report(a.err_flag, KVQ_DEV_BAD_POS);
+        return;
+    }
+    const int64_t page = slot >> 2;
+    const bool keep = slot >= 0 && page < a.num_pages;
+    if (slot >= 0 && !keep && chunk == 0 && lane == 0) report(a.err_flag, KVQ_DEV_BAD_SLOT);
+
+    uint4 raw[kIter];
+    int head[kIter];
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) {
+        const int h = (chunk * kIter + i) * a.heads_per_warp + sub;
+        head[i] = live && h < heads ? h : -1;
+        raw[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (head[i] < 0) continue;
+        const int hk = h - a.num_q_heads, hv = hk - a.num_kv_heads;
+        const __half *src = hk < 0 ? a.q + token * a.q_stride + (int64_t)h * a.head_dim
+                                   : hv < 0 ? a.k + token * a.k_stride + (int64_t)hk * a.head_dim
+                                            : a.v + token * a.v_stride + (int64_t)hv * a.head_dim;
+        raw[i] = *reinterpret_cast<const uint4 *>(src + ch);
+    }
+    // this lane's table entries: out = fl(x c) + fl(partner s), s carrying the sign
+    float c[8], s[8];
+    const int half = a.rot_dim / 2;
+    const bool turns = ROTATE && ch < a.rot_dim;
+    if (turns) {
+        const float *row = a.table + (int64_t)pos * a.rot_dim;
+        if (a.interleaved) {
+            const float4 cc = __ldg(reinterpret_cast<const float4 *>(row + ch / 2));
+            const float4 ss = __ldg(reinterpret_cast<const float4 *>(row + half + ch / 2));
+            const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                c[j] = cv[j / 2];
+                s[j] = (j & 1) ? sv[j / 2] : -sv[j / 2];
+            }
+        } else {
+            const bool first = ch < half;
+            const int at = first ? ch : ch - half;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const float4 cc = __ldg(reinterpret_cast<const float4 *>(row + at) + q);
+                const float4 ss = __ldg(reinterpret_cast<const float4 *>(row + half + at) + q);
+                const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    c[4 * q + j] = cv[j];
+                    s[4 * q + j] = first ? -sv[j] : sv[j];
+                }
+            }
+        }
+    }
+    const int mate = a.interleaved || !turns ? lane : (ch < half ? lane + half / 8 : lane - half / 8);
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) {
+        uint4 other = raw[i];
+        if (ROTATE && !a.interleaved) {
+            other.x = __shfl_sync(kAll, raw[i].x, mate);
+            other.y = __shfl_sync(kAll, raw[i].y, mate);
+            other.z = __shfl_sync(kAll, raw[i].z, mate);
+            other.w = __shfl_sync(kAll, raw[i].w, mate);
+        }
+        const int h = head[i], hk = h - a.num_q_heads, hv = hk - a.num_kv_heads;
+        float x[8];
+        unpack8(raw[i], x);
+        if (turns && hv < 0) {
+            float p[8];
+            unpack8(other, p);
+            if (a.interleaved) {
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {
+                    const float t = p[j];
+                    p[j] = p[j + 1];
+                    p[j + 1] = t;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = __fadd_rn(__fmul_rn(x[j], c[j]), __fmul_rn(p[j], s[j]));
+        }
+        if (POOL == PoolKind::e2m1) {
+            // the block of 16: this lane's eight channels and its neighbour's
+            uint32_t m = 0u;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(x[j]) & 0x7FFFFFFFu);
+            m = max(m, __shfl_xor_sync(kAll, m, 1));
+            if (hk >= 0 && keep) {
+                const float scale = hv < 0 ? a.k_scale : a.v_scale;
+                const E2m1Block blk = e2m1_block(m, hv < 0 ? a.k_six : a.v_six, scale);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(x[j], blk.factor);
+                uint8_t *dst = static_cast<uint8_t *>(hv < 0 ? a.k_cache : a.v_cache) +
+                               (page * a.num_kv_heads + (hv < 0 ? hk : hv)) * e2m1_page_bytes(a.head_dim);
+                *reinterpret_cast<uint32_t *>(dst + (slot & 3) * (a.head_dim / 2) + ch / 2) = e2m1_pack8(x);
+                if ((vec & 1) == 0) dst[e2m1_scale_off(a.head_dim) + (ch / 16) * 4 + (slot & 3)] = (uint8_t)blk.scale;
+            }
+        }
+        if (h < 0) continue;
+        if (hk < 0) {
+            *reinterpret_cast<uint4 *>(a.q_out + (token * a.num_q_heads + h) * a.head_dim + ch) = pack8(x);
+        } else if (POOL != PoolKind::e2m1 && keep) {
+            const int64_t at = ((page * a.num_kv_heads + (hv < 0 ? hk : hv)) * 4 + (slot & 3)) * a.head_dim + ch;
+            void *pool = hv < 0 ? a.k_cache : a.v_cache;
+            if (POOL == PoolKind::e4m3)
+                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(pool) + at) = quantize8(x, hv < 0 ? a.k_scale : a.v_scale);
+            else
+                *reinterpret_cast<uint4 *>(static_cast<__half *>(pool) + at) = pack8(x);
+        }
+    }
+}
+
+cudaError_t launch_append_rope(PoolKind pool, bool rotate, RopeArgs a, cudaStream_t stream)
+{
+    a.lanes = a.head_dim / 8;
+    a.heads_per_warp = 32 / a.lanes;
+    const int heads = a.num_q_heads + 2 * a.num_kv_heads;
+    const int groups = (heads + a.heads_per_warp - 1) / a.heads_per_warp;
+    a.chunks = (groups + kIter - 1) / kIter;
+    const int64_t warps = (int64_t)a.num_tokens * a.chunks;
+    const int64_t blocks = (warps * 32 + kRopeThreads - 1) / kRopeThreads;
+    if (blocks == 0) return cudaSuccess;
+    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    const dim3 grid((unsigned)blocks), block(kRopeThreads);
+    if (!rotate) return launch_pdl(append_rope_kernel<PoolKind::e2m1, false>, grid, block, 0, stream, a);
+    if (pool == PoolKind::e2m1) return launch_pdl(append_rope_kernel<PoolKind::e2m1, true>, grid, block, 0, stream, a);
+    if (pool == PoolKind::e4m3) return launch_pdl(append_rope_kernel<PoolKind::e4m3, true>, grid, block, 0, stream, a);
+    return launch_pdl(append_rope_kernel<PoolKind::fp16, true>, grid, block, 0, stream, a);
+}
+
+// ---------------------------------------------------------------------------
+// Read-back: the rows of the listed slots as fp16, fl16(fl32(E2M1 * b) * S);
+// E2M1 * b has at most 6 significant bits, so the product with S is the only
+// binary32 rounding.  One thread per 8 channels of K or V (blockIdx.y).
+__global__ void __launch_bounds__(256) gather_e2m1_kernel(const uint8_t *__restrict__ k_cache,
+                                                          const uint8_t *__restrict__ v_cache, int64_t num_pages,
+                                                          const int32_t *__restrict__ slots, int64_t num_vecs,
+                                                          int num_kv_heads, int head_dim, float k_scale, float v_scale,
+                                                          __half *__restrict__ k_out, __half *__restrict__ v_out,
+                                                          int32_t *err_flag)
+{
+    grid_dependency_wait();   // the preceding kernel may write the pools
+    launch_dependents();
+    const int64_t j = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (j >= num_vecs) return;
+    const bool is_v = blockIdx.y != 0;
+    const int vph = head_dim / 8;
+    const int64_t row = j / vph;                       // (token, kv head)
+    const int vec = (int)(j - row * vph);
+    const int64_t token = row / num_kv_heads;
+    const int g = (int)(row - token * num_kv_heads);
+    const int32_t slot = __ldg(slots + token);
+    const int64_t page = slot >> 2;
+    float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (slot >= 0 && page < num_pages) {
+        const uint8_t *src = (is_v ? v_cache : k_cache) + (page * num_kv_heads + g) * e2m1_page_bytes(head_dim);
+        const uint32_t code = *reinterpret_cast<const uint32_t *>(src + (slot & 3) * (head_dim / 2) + vec * 4);
+        const uint32_t b = src[e2m1_scale_off(head_dim) + (vec / 2) * 4 + (slot & 3)];
+        const float block = e4m3_value(b), scale = is_v ? v_scale : k_scale;
+        const uint32_t h[4] = {e2m1_pair<0>(code), e2m1_pair<1>(code), e2m1_pair<2>(code), e2m1_pair<3>(code)};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+            y[2 * i] = __fmul_rn(__fmul_rn(f.x, block), scale);
+            y[2 * i + 1] = __fmul_rn(__fmul_rn(f.y, block), scale);
+        }
+    } else if (slot >= 0 && g == 0 && vec == 0 && !is_v) {
+        report(err_flag, KVQ_DEV_BAD_SLOT);
+    }
+    *reinterpret_cast<uint4 *>((is_v ? v_out : k_out) + row * head_dim + vec * 8) = pack8(y);
+}
+
+cudaError_t launch_gather_e2m1(const void *k_cache, const void *v_cache, int64_t num_pages, const int32_t *slots,
+                               int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim, float k_scale, float v_scale,
+                               void *k_out, void *v_out, int32_t *err_flag, cudaStream_t stream)
+{
+    const int64_t n = (int64_t)num_tokens * num_kv_heads * (head_dim / 8);
+    if (n == 0) return cudaSuccess;
+    const int64_t blocks = (n + 255) / 256;
+    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    return launch_pdl(gather_e2m1_kernel, dim3((unsigned)blocks, 2), dim3(256), 0, stream,
+                      static_cast<const uint8_t *>(k_cache), static_cast<const uint8_t *>(v_cache), num_pages, slots, n,
+                      num_kv_heads, head_dim, k_scale, v_scale, static_cast<__half *>(k_out), static_cast<__half *>(v_out),
+                      err_flag);
+}
+
+// ---------------------------------------------------------------------------
+// The rotation table, one thread per (position, pair): angles in binary64 (at
+// position 262,143 a binary32 angle is off by up to 2^-7 radians), rounded to
+// binary32 after cos and sin.  Made once when a model is loaded.
+__global__ void __launch_bounds__(256) rope_table_kernel(float *__restrict__ table, int32_t max_positions, int32_t half,
+                                                         double base, int32_t kind, double factor, double low, double high,
+                                                         double magnitude)
+{
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= (int64_t)max_positions * half) return;
+    const int64_t p = i / half;
+    const int j = (int)(i - p * half);
+    double f = pow(base, -(double)j / half);
+    if (kind == KVQ_ROPE_LINEAR) f /= factor;
+    if (kind == KVQ_ROPE_YARN) {
+        const double ramp = fmin(fmax((j - low) / (high - low), 0.0), 1.0);
+        f = f / factor * ramp + f * (1.0 - ramp);
+    }
+    double sn, cs;
+    sincos((double)p * f, &sn, &cs);
+    table[p * 2 * half + j] = (float)(cs * magnitude);
+    table[p * 2 * half + half + j] = (float)(sn * magnitude);
+}
+
+cudaError_t launch_rope_table(float *table, int32_t max_positions, int32_t rot_dim, double base, int32_t kind, double factor,
+                              double low, double high, double magnitude, cudaStream_t stream)
+{
+    const int64_t n = (int64_t)max_positions * (rot_dim / 2);
+    const int64_t blocks = (n + 255) / 256;
+    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    rope_table_kernel<<<(unsigned)blocks, 256, 0, stream>>>(table, max_positions, rot_dim / 2, base, kind, factor, low, high,
+                                                            magnitude);
+    return cudaGetLastError();
+}
+
+}  // namespace kvq

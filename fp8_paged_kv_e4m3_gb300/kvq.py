@@ -23,12 +23,14 @@ PAGE_SIZE = 4
 KVQ_OK = 0
 STATUS = {0: "ok", -1: "invalid argument", -2: "bad scale", -3: "workspace", -4: "unsupported",
           -5: "CUDA error", -6: "alignment"}
-DEV_BAD_PAGE, DEV_BAD_SLOT, DEV_BAD_TOPK, DEV_BAD_LEN, DEV_TIMEOUT = 1, 2, 4, 8, 16
+DEV_BAD_PAGE, DEV_BAD_SLOT, DEV_BAD_TOPK, DEV_BAD_LEN, DEV_TIMEOUT, DEV_BAD_POS = 1, 2, 4, 8, 16, 32
 ATTN_BITCAST_DECODE = 1
 ATTN_MMA_SYNC = 2
 ATTN_FP8_QK = 4
 ATTN_STRICT_ORDER = 8
 ATTN_LONGEST_FIRST = 32
+ROPE_INTERLEAVED = 1
+ROPE_SCALING = {None: 0, "linear": 1, "yarn": 2}
 
 _lock = threading.Lock()
 _lib = None
@@ -56,13 +58,22 @@ class PrefillParams(ctypes.Structure):
                 ("total_q", ctypes.c_int32), ("sm_scale", ctypes.c_float), ("flags", ctypes.c_int32)]
 
 
+class RopeParams(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("max_positions", ctypes.c_int32), ("flags", ctypes.c_int32),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64)]
+
+
 EXPORTS = ("kvq_version", "kvq_status_string", "kvq_validate_scales", "kvq_amax_f16",
            "kvq_scale_from_amax", "kv_append_e4m3", "kv_append_fp16", "kvq_attn_num_splits",
            "kvq_attn_workspace_bytes", "paged_decode_attn_e4m3", "paged_decode_attn_fp16",
            "paged_decode_attn_e4m3_partial", "paged_decode_attn_fp16_partial", "kvq_lse_combine",
            "paged_decode_step_e4m3", "paged_decode_step_fp16", "kvq_attn_launches",
            "paged_decode_attn_e4m3_noalloc", "kvq_prefill_workspace_bytes", "paged_prefill_attn_e4m3",
-           "paged_prefill_attn_fp16")
+           "paged_prefill_attn_fp16", "kvq_rope_table", "kv_append_rope_e4m3", "kv_append_rope_fp16",
+           "kv_append_rope_e2m1", "kvq_scale_from_amax_e2m1", "kv_append_e2m1", "kv_gather_e2m1",
+           "paged_decode_attn_e2m1", "paged_decode_attn_e2m1_partial", "paged_prefill_attn_e2m1")
 
 
 def load(path: Optional[str] = None):
@@ -106,11 +117,26 @@ def load(path: Optional[str] = None):
         lib.kvq_prefill_workspace_bytes.restype = sz
         lib.paged_prefill_attn_e4m3.argtypes = [V, V, V, i64, V, V, V, f32, f32, V, sz, V, PP, V, V]
         lib.paged_prefill_attn_fp16.argtypes = [V, V, V, i64, V, V, V, V, sz, V, PP, V, V]
+        PR, f64 = ctypes.POINTER(RopeParams), ctypes.c_double
+        lib.kvq_scale_from_amax_e2m1.argtypes = [f32]
+        lib.kvq_scale_from_amax_e2m1.restype = f32
+        lib.kvq_rope_table.argtypes = [V, i32, i32, f64, i32, f64, i32, f64, f64, f64, V]
+        lib.kv_append_rope_e4m3.argtypes = [V, V, V, V, V, V, V, V, V, i64, f32, f32, PR, V, V]
+        lib.kv_append_rope_fp16.argtypes = [V, V, V, V, V, V, V, V, V, i64, PR, V, V]
+        lib.kv_append_rope_e2m1.argtypes = lib.kv_append_rope_e4m3.argtypes
+        lib.kv_append_e2m1.argtypes = lib.kv_append_e4m3.argtypes
+        lib.kv_gather_e2m1.argtypes = [V, V, i64, V, i32, i32, i32, f32, f32, V, V, V, V]
+        lib.paged_decode_attn_e2m1.argtypes = lib.paged_decode_attn_e4m3.argtypes
+        lib.paged_decode_attn_e2m1_partial.argtypes = lib.paged_decode_attn_e4m3_partial.argtypes
+        lib.paged_prefill_attn_e2m1.argtypes = lib.paged_prefill_attn_e4m3.argtypes
         for name in ("kvq_validate_scales", "kvq_amax_f16", "kv_append_e4m3", "kv_append_fp16",
                      "paged_decode_attn_e4m3", "paged_decode_attn_fp16",
                      "paged_decode_attn_e4m3_partial", "paged_decode_attn_fp16_partial",
                      "kvq_lse_combine", "paged_decode_step_e4m3", "paged_decode_step_fp16",
-                     "paged_prefill_attn_e4m3", "paged_prefill_attn_fp16"):
+                     "paged_prefill_attn_e4m3", "paged_prefill_attn_fp16", "kvq_rope_table",
+                     "kv_append_rope_e4m3", "kv_append_rope_fp16", "kv_append_rope_e2m1", "kv_append_e2m1",
+                     "kv_gather_e2m1", "paged_decode_attn_e2m1", "paged_decode_attn_e2m1_partial",
+                     "paged_prefill_attn_e2m1"):
             getattr(lib, name).restype = ctypes.c_int
         if path is None:
             _lib = lib
@@ -279,16 +305,33 @@ def workspace_views(ws: torch.Tensor, p: AttnParams):
             ws[l_off:l_off + units].view(shp))
 
 
+def e2m1_page_bytes(head_dim: int) -> int:
+    """Bytes of one E2M1 page of one kv head: 4 tokens' codes and block scales."""
+    return 9 * head_dim // 4
+
+
+def _pools(k_cache, v_cache, dtype, D: int, e2m1: bool = False) -> int:
+    """Check a K and a V pool of head_dim D; returns the kv heads."""
+    tail = (e2m1_page_bytes(D),) if e2m1 else (PAGE_SIZE, D)
+    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _need(c, name, dtype, 2 + len(tail))
+        if c.shape != k_cache.shape or tuple(c.shape[2:]) != tail:
+            raise ValueError(f"caches must be [P, Hkv, {', '.join(map(str, tail))}]")
+    return k_cache.shape[1]
+
+
+def _same_device(like: torch.Tensor, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != like.device:
+            raise ValueError(f"{name}: on {t.device}, expected {like.device}")
+
+
 def _attn_check(q, k_cache, v_cache, block_tables, context_lens, workspace, out, topk_idx,
                 topk_lens, cache_dtype, num_splits_, sm_scale, split_pages, bitcast_decode=False,
-                mma_sync=False, fp8_qk=False, strict_order=False, longest_first=False):
+                mma_sync=False, fp8_qk=False, strict_order=False, longest_first=False, e2m1=False):
     _need(q, "q", torch.float16, 4)
     B, q_len, Hq, D = q.shape
-    _need(k_cache, "k_cache", cache_dtype, 4)
-    _need(v_cache, "v_cache", cache_dtype, 4)
-    if k_cache.shape != v_cache.shape or k_cache.shape[2:] != (PAGE_SIZE, D):
-        raise ValueError(f"caches must be [P, Hkv, {PAGE_SIZE}, {D}]")
-    Hkv = k_cache.shape[1]
+    Hkv = _pools(k_cache, v_cache, cache_dtype, D, e2m1)
     _need(block_tables, "block_tables", torch.int32, 2)
     _need(context_lens, "context_lens", torch.int32, 1)
     if block_tables.shape[0] != B or context_lens.shape[0] != B:
@@ -467,13 +510,10 @@ def alloc_prefill_workspace(p: PrefillParams, device) -> torch.Tensor:
 
 
 def _prefill_check(q, k_cache, v_cache, block_tables, context_lens, q_start, workspace, out,
-                   cache_dtype, max_q_len, sm_scale):
+                   cache_dtype, max_q_len, sm_scale, e2m1=False):
     _need(q, "q", torch.float16, 3)
     Tq, Hq, D = q.shape
-    _need(k_cache, "k_cache", cache_dtype, 4)
-    _need(v_cache, "v_cache", cache_dtype, 4)
-    if k_cache.shape != v_cache.shape or k_cache.shape[2:] != (PAGE_SIZE, D):
-        raise ValueError(f"caches must be [P, Hkv, {PAGE_SIZE}, {D}]")
+    _pools(k_cache, v_cache, cache_dtype, D, e2m1)
     _need(block_tables, "block_tables", torch.int32, 2)
     _need(context_lens, "context_lens", torch.int32, 1)
     _need(q_start, "q_start", torch.int32, 1)
@@ -517,4 +557,231 @@ def paged_prefill_attn_fp16(q, k_cache, v_cache, block_tables, context_lens, q_s
         _ptr(q), _ptr(k_cache), _ptr(v_cache), k_cache.shape[0], _ptr(block_tables), _ptr(context_lens),
         _ptr(q_start), _ptr(workspace), workspace.numel(), _ptr(out), ctypes.byref(p), _ptr(err_flag),
         _stream(q)))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# rotary positions, and the append with the rotation on the way
+
+def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, scaling: Optional[str] = None,
+               factor: float = 1.0, original_positions: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+               magnitude: float = 0.0, device="cuda") -> torch.Tensor:
+    """The float32 [max_positions, rot_dim] table (cos, then sin, of every
+    position's angles) that the kv_append_rope_* calls read.  scaling: None,
+    "linear" (factor) or "yarn" (factor, original_positions, beta_fast,
+    beta_slow); magnitude 0 = 1, or 0.1 ln(factor) + 1 with "yarn"."""
+    if scaling not in ROPE_SCALING:
+        raise ValueError(f"scaling: expected one of {list(ROPE_SCALING)}")
+    if max_positions < 1 or rot_dim < 1 or rot_dim % 16:
+        raise ValueError("max_positions and rot_dim must be positive, rot_dim a multiple of 16")
+    table = torch.empty(max_positions, rot_dim, dtype=torch.float32, device=device)
+    with torch.cuda.device(table.device):
+        _check("kvq_rope_table", load().kvq_rope_table(
+            _ptr(table), max_positions, rot_dim, base, ROPE_SCALING[scaling], factor, original_positions, beta_fast,
+            beta_slow, magnitude, _stream(table)))
+    return table
+
+
+def _heads(t, name: str):
+    """An fp16 [T, H, D] CUDA tensor whose heads are contiguous; any token stride (a slice of a packed
+    projection).  Returns the stride in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.dtype != torch.float16:
+        raise TypeError(f"{name}: expected {torch.float16}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name}: expected 3 dims, got {tuple(t.shape)}")
+    T, H, D = t.shape
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if T <= 1:
+        return H * D
+    if t.stride(0) < H * D:
+        raise ValueError(f"{name}: tokens overlap")
+    return t.stride(0)
+
+
+def _append_rope(fn, q, k_new, v_new, positions, table, slot_mapping, k_cache, v_cache, scales, dtype, e2m1, q_out,
+                 interleaved, err_flag):
+    ks, vs = _heads(k_new, "k_new"), _heads(v_new, "v_new")
+    if k_new.shape != v_new.shape:
+        raise ValueError("k_new and v_new shapes differ")
+    T, Hkv, D = k_new.shape
+    Hq = qs = 0
+    if q is not None:
+        qs = _heads(q, "q")
+        Hq = q.shape[1]
+        if q.shape[0] != T or q.shape[2] != D or Hq < 1:
+            raise ValueError(f"q must be [{T}, Hq, {D}], got {tuple(q.shape)}")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        _need(q_out, "q_out", torch.float16, 3)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have the shape of q")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _need(positions, "positions", torch.int32, 1)
+    _need(slot_mapping, "slot_mapping", torch.int32, 1)
+    if positions.numel() != T or slot_mapping.numel() != T:
+        raise ValueError("positions / slot_mapping length != number of tokens")
+    _need(table, "table", torch.float32, 2)
+    if _pools(k_cache, v_cache, dtype, D, e2m1) != Hkv:
+        raise ValueError(f"the pools hold {k_cache.shape[1]} kv heads, k_new has {Hkv}")
+    if err_flag is not None:
+        _need(err_flag, "err_flag", torch.int32)
+    _same_device(k_new, q=q, q_out=q_out, v_new=v_new, positions=positions, table=table, slot_mapping=slot_mapping,
+                 k_cache=k_cache, v_cache=v_cache, err_flag=err_flag)
+    p = RopeParams(T, Hq, Hkv, D, table.shape[1], table.shape[0], ROPE_INTERLEAVED if interleaved else 0, qs, ks, vs)
+    with torch.cuda.device(k_new.device):
+        _check(fn, getattr(load(), fn)(
+            _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(positions), _ptr(table), _ptr(slot_mapping), _ptr(q_out),
+            _ptr(k_cache), _ptr(v_cache), k_cache.shape[0], *[ctypes.c_float(s) for s in scales], ctypes.byref(p),
+            _ptr(err_flag), _stream(k_new)))
+    return q_out
+
+
+def kv_append_rope_e4m3(q, k_new, v_new, positions, table, slot_mapping, k_cache, v_cache, k_scale: float, v_scale: float,
+                        q_out=None, interleaved: bool = False, err_flag: Optional[torch.Tensor] = None):
+    """Rotate q [T, Hq, D] (None: no queries) and k_new [T, Hkv, D] by their
+    positions and append K and V to uint8 (E4M3) pools, in one launch.
+    table: rope_table(...), whose width is the rotated part of the head.
+    interleaved: pairs (2j, 2j + 1) instead of (j, j + rot_dim / 2).  q, k_new
+    and v_new may be slices of one packed projection; q_out may be q itself
+    when that is contiguous.  Returns q_out."""
+    return _append_rope("kv_append_rope_e4m3", q, k_new, v_new, positions, table, slot_mapping, k_cache, v_cache,
+                        (k_scale, v_scale), torch.uint8, False, q_out, interleaved, err_flag)
+
+
+def kv_append_rope_fp16(q, k_new, v_new, positions, table, slot_mapping, k_cache, v_cache, q_out=None,
+                        interleaved: bool = False, err_flag: Optional[torch.Tensor] = None):
+    """fp16-KV twin of kv_append_rope_e4m3."""
+    return _append_rope("kv_append_rope_fp16", q, k_new, v_new, positions, table, slot_mapping, k_cache, v_cache, (),
+                        torch.float16, False, q_out, interleaved, err_flag)
+
+
+def kv_append_rope_e2m1(q, k_new, v_new, positions, table, slot_mapping, k_cache, v_cache, k_scale: float, v_scale: float,
+                        q_out=None, interleaved: bool = False, err_flag: Optional[torch.Tensor] = None):
+    """kv_append_rope_e4m3 into E2M1 pools."""
+    return _append_rope("kv_append_rope_e2m1", q, k_new, v_new, positions, table, slot_mapping, k_cache, v_cache,
+                        (k_scale, v_scale), torch.uint8, True, q_out, interleaved, err_flag)
+
+
+# ---------------------------------------------------------------------------
+# the 4-bit cache
+
+def scale_from_amax_e2m1(amax: float) -> float:
+    return float(load().kvq_scale_from_amax_e2m1(ctypes.c_float(amax)))
+
+
+def calibrate_scale_e2m1(x: torch.Tensor) -> float:
+    """scale = amax / 2688 of a calibration draw (synchronises to read amax)."""
+    return scale_from_amax_e2m1(float(amax_f16(x).item()))
+
+
+def alloc_e2m1_pool(num_pages: int, num_kv_heads: int, head_dim: int, device="cuda") -> torch.Tensor:
+    """A zeroed E2M1 pool, uint8 [num_pages, num_kv_heads, 9 * head_dim / 4]."""
+    return torch.zeros(num_pages, num_kv_heads, e2m1_page_bytes(head_dim), dtype=torch.uint8, device=device)
+
+
+def kv_append_e2m1(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale: float, v_scale: float,
+                   err_flag: Optional[torch.Tensor] = None) -> None:
+    """Quantise fp16 K/V of new tokens [T, Hkv, D] into E2M1 pools."""
+    _need(k_new, "k_new", torch.float16, 3)
+    _need(v_new, "v_new", torch.float16, 3)
+    if k_new.shape != v_new.shape:
+        raise ValueError("k_new and v_new shapes differ")
+    T, Hkv, D = k_new.shape
+    _need(slot_mapping, "slot_mapping", torch.int32, 1)
+    if slot_mapping.numel() != T:
+        raise ValueError("slot_mapping length != number of tokens")
+    if _pools(k_cache, v_cache, torch.uint8, D, True) != Hkv:
+        raise ValueError(f"the pools hold {k_cache.shape[1]} kv heads, k_new has {Hkv}")
+    if err_flag is not None:
+        _need(err_flag, "err_flag", torch.int32)
+    _same_device(k_new, v_new=v_new, slot_mapping=slot_mapping, k_cache=k_cache, v_cache=v_cache, err_flag=err_flag)
+    with torch.cuda.device(k_new.device):
+        _check("kv_append_e2m1", load().kv_append_e2m1(
+            _ptr(k_new), _ptr(v_new), _ptr(slot_mapping), T, Hkv, D, _ptr(k_cache), _ptr(v_cache), k_cache.shape[0],
+            ctypes.c_float(k_scale), ctypes.c_float(v_scale), _ptr(err_flag), _stream(k_new)))
+
+
+def kv_gather_e2m1(k_cache, v_cache, slots, k_scale: float, v_scale: float, k_out=None, v_out=None,
+                   err_flag: Optional[torch.Tensor] = None):
+    """The cached rows at `slots` as fp16 [T, Hkv, D] (K, V); zeros for a slot of -1."""
+    _need(k_cache, "k_cache", torch.uint8, 3)
+    D = k_cache.shape[2] * 4 // 9
+    Hkv = _pools(k_cache, v_cache, torch.uint8, D, True)
+    _need(slots, "slots", torch.int32, 1)
+    shape = (slots.numel(), Hkv, D)
+    k_out, v_out = (torch.empty(shape, dtype=torch.float16, device=k_cache.device) if t is None else t
+                    for t in (k_out, v_out))
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        _need(t, name, torch.float16, 3)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name}: expected {shape}, got {tuple(t.shape)}")
+    if err_flag is not None:
+        _need(err_flag, "err_flag", torch.int32)
+    _same_device(k_cache, v_cache=v_cache, slots=slots, k_out=k_out, v_out=v_out, err_flag=err_flag)
+    with torch.cuda.device(k_cache.device):
+        _check("kv_gather_e2m1", load().kv_gather_e2m1(
+            _ptr(k_cache), _ptr(v_cache), k_cache.shape[0], _ptr(slots), slots.numel(), Hkv, D, ctypes.c_float(k_scale),
+            ctypes.c_float(v_scale), _ptr(k_out), _ptr(v_out), _ptr(err_flag), _stream(k_cache)))
+    return k_out, v_out
+
+
+def _e2m1_devices(q, **tensors):
+    if tensors.get("err_flag") is not None:
+        _need(tensors["err_flag"], "err_flag", torch.int32)
+    _same_device(q, **tensors)
+
+
+def paged_decode_attn_e2m1(q, k_cache, v_cache, block_tables, context_lens, k_scale: float, v_scale: float, workspace,
+                           out=None, topk_idx=None, topk_lens=None, num_splits: int = 0, sm_scale: float = 0.0,
+                           err_flag=None, split_pages: int = 0, strict_order: bool = False):
+    """paged_decode_attn_e4m3 over E2M1 pools [P, Hkv, 9 * D / 4]; returns `out` (fp16, shape of q)."""
+    p = _attn_check(q, k_cache, v_cache, block_tables, context_lens, workspace, out, topk_idx, topk_lens, torch.uint8,
+                    num_splits, sm_scale, split_pages, strict_order=strict_order, e2m1=True)
+    _e2m1_devices(q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, context_lens=context_lens,
+                  workspace=workspace, out=out, topk_idx=topk_idx, topk_lens=topk_lens, err_flag=err_flag)
+    if out is None:
+        out = torch.empty_like(q)
+    with torch.cuda.device(q.device):
+        _check("paged_decode_attn_e2m1", load().paged_decode_attn_e2m1(
+            _ptr(q), _ptr(k_cache), _ptr(v_cache), k_cache.shape[0], _ptr(block_tables), _ptr(context_lens),
+            ctypes.c_float(k_scale), ctypes.c_float(v_scale), _ptr(topk_idx), _ptr(topk_lens), _ptr(workspace),
+            workspace.numel() * 4, _ptr(out), ctypes.byref(p), _ptr(err_flag), _stream(q)))
+    return out
+
+
+def paged_decode_attn_e2m1_partial(q, k_cache, v_cache, block_tables, context_lens, k_scale: float, v_scale: float,
+                                   workspace, topk_idx=None, topk_lens=None, num_splits: int = 0, sm_scale: float = 0.0,
+                                   err_flag=None, split_pages: int = 0, strict_order: bool = False) -> AttnParams:
+    p = _attn_check(q, k_cache, v_cache, block_tables, context_lens, workspace, None, topk_idx, topk_lens, torch.uint8,
+                    num_splits, sm_scale, split_pages, strict_order=strict_order, e2m1=True)
+    _e2m1_devices(q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, context_lens=context_lens,
+                  workspace=workspace, topk_idx=topk_idx, topk_lens=topk_lens, err_flag=err_flag)
+    with torch.cuda.device(q.device):
+        _check("paged_decode_attn_e2m1_partial", load().paged_decode_attn_e2m1_partial(
+            _ptr(q), _ptr(k_cache), _ptr(v_cache), k_cache.shape[0], _ptr(block_tables), _ptr(context_lens),
+            ctypes.c_float(k_scale), ctypes.c_float(v_scale), _ptr(topk_idx), _ptr(topk_lens), _ptr(workspace),
+            workspace.numel() * 4, ctypes.byref(p), _ptr(err_flag), _stream(q)))
+    return p
+
+
+def paged_prefill_attn_e2m1(q, k_cache, v_cache, block_tables, context_lens, q_start, k_scale: float, v_scale: float,
+                            workspace, out=None, max_q_len: Optional[int] = None, sm_scale: float = 0.0, err_flag=None):
+    """paged_prefill_attn_e4m3 over E2M1 pools [P, Hkv, 288]."""
+    p = _prefill_check(q, k_cache, v_cache, block_tables, context_lens, q_start, workspace, out, torch.uint8, max_q_len,
+                       sm_scale, e2m1=True)
+    _e2m1_devices(q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, context_lens=context_lens,
+                  q_start=q_start, workspace=workspace, out=out, err_flag=err_flag)
+    if out is None:
+        out = torch.empty_like(q)
+    with torch.cuda.device(q.device):
+        _check("paged_prefill_attn_e2m1", load().paged_prefill_attn_e2m1(
+            _ptr(q), _ptr(k_cache), _ptr(v_cache), k_cache.shape[0], _ptr(block_tables), _ptr(context_lens),
+            _ptr(q_start), ctypes.c_float(k_scale), ctypes.c_float(v_scale), _ptr(workspace), workspace.numel(),
+            _ptr(out), ctypes.byref(p), _ptr(err_flag), _stream(q)))
     return out

@@ -77,9 +77,10 @@ enum {
     KVQ_DEV_BAD_SLOT = 2,   /* append slot beyond the pool: token not written           */
     KVQ_DEV_BAD_TOPK = 4,   /* top-k index outside [0, context_len): entry skipped      */
     KVQ_DEV_BAD_LEN = 8,    /* context_len < q_len or > 4 * max_pages_per_seq: row = 0   */
-    KVQ_DEV_TIMEOUT = 16    /* an internal pipeline wait gave up (~2 s): results invalid;
+    KVQ_DEV_TIMEOUT = 16,   /* an internal pipeline wait gave up (~2 s): results invalid;
                                the CTA that gave up drained its copies, wrote its split
                                partials as empty (m = -inf, l = 0) and exited            */
+    KVQ_DEV_BAD_POS = 32    /* rotary position outside [0, max_positions): token skipped */
 };
 
 /* Library version (KVQ_VERSION) and a static string for a status code. */
@@ -443,6 +444,145 @@ int paged_prefill_attn_fp16(const void *q, const void *k_cache, const void *v_ca
                             int64_t num_pages, const int32_t *block_tables,
                             const int32_t *context_lens, const int32_t *q_start,
                             void *workspace, size_t workspace_bytes, void *out,
+                            const kvq_prefill_params *p, int32_t *err_flag, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions.  Pair j (0 <= j < rot_dim / 2) of a token at position p is
+ * turned by the angle p * f_j, f_j = base^(-2 j / rot_dim).
+ *
+ * kvq_rope_table fills the table the appends below read: table[p][j] =
+ * magnitude * cos(p f_j), table[p][rot_dim / 2 + j] = magnitude * sin(p f_j),
+ * angles in binary64, entries rounded to binary32.  Scaling for contexts
+ * longer than a model was trained on:
+ *   KVQ_ROPE_NONE    f_j as above
+ *   KVQ_ROPE_LINEAR  f_j / factor (position interpolation)
+ *   KVQ_ROPE_YARN    interpolation by parts (YaRN, Peng et al. 2023): with
+ *     d(beta) = rot_dim ln(original_positions / (2 pi beta)) / (2 ln base),
+ *     low = max(floor(d(beta_fast)), 0), high = min(ceil(d(beta_slow)),
+ *     rot_dim - 1), r_j = (j - low) / (high - low) clamped to [0, 1]:
+ *     f_j (1 - r_j) + f_j r_j / factor
+ *   table : device float32 [max_positions][rot_dim]; rot_dim a multiple of 16
+ *   base > 1; factor >= 1 (LINEAR, YARN); original_positions >= 1 and
+ *   0 < beta_slow < beta_fast (YARN)
+ *   magnitude : 0 = 1, or 0.1 ln(factor) + 1 with YARN
+ * One kernel on `stream`; made once, when a model is loaded.
+ */
+enum { KVQ_ROPE_NONE = 0, KVQ_ROPE_LINEAR = 1, KVQ_ROPE_YARN = 2 };
+
+int kvq_rope_table(float *table, int32_t max_positions, int32_t rot_dim, double base, int32_t scaling, double factor,
+                   int32_t original_positions, double beta_fast, double beta_slow, double magnitude, void *stream);
+
+/* Rotate the queries and keys of new tokens, and append: one launch in place
+ * of a rotation of q, a rotation of k and kv_append_*.
+ *
+ * For token t at positions[t] with c, s its table entries, every channel pair
+ * (x1, x2) of each query and key head becomes, in binary32 (each product and
+ * sum rounded to nearest even),
+ *     y1 = x1 c - x2 s,   y2 = x2 c + x1 s
+ * where pair j is channels (j, j + rot_dim / 2), or (2 j, 2 j + 1) with
+ * KVQ_ROPE_INTERLEAVED; channels from rot_dim on are unchanged.  Queries are
+ * rounded to fp16 into q_out.  Keys go from the binary32 values to the pool's
+ * type with one rounding (kv_append_* after a rotation to fp16 would round
+ * twice), values as in the plain append.
+ *   q, k_new, v_new : device fp16, token t's heads at t * *_stride elements,
+ *                  [heads][head_dim] contiguous: slices of one packed
+ *                  projection are accepted.  16-B aligned, strides multiples
+ *                  of 8.  q may be NULL with num_q_heads 0.
+ *   positions    : device int32 [num_tokens]; outside [0, max_positions) sets
+ *                  KVQ_DEV_BAD_POS and skips the token: neither q_out's row
+ *                  nor the pools are written
+ *   table        : device float32 [max_positions][rot_dim], 16-B aligned
+ *   slot_mapping : as for kv_append_e4m3 (-1 = not appended; its query is
+ *                  rotated all the same); slots >= 0 are distinct
+ *   q_out        : device fp16 [num_tokens][num_q_heads][head_dim], 16-B
+ *                  aligned; may be q itself when q is packed, and otherwise
+ *                  overlaps no input
+ *   pools, scales, err_flag : as for the plain append of the pool's type
+ * head_dim a multiple of 16 up to 256 (E2M1: 64 or 128), rot_dim a multiple
+ * of 16 up to head_dim; otherwise KVQ_ERR_UNSUPPORTED.
+ */
+#define KVQ_ROPE_INTERLEAVED 1
+
+typedef struct {
+    int32_t num_tokens;
+    int32_t num_q_heads;    /* 0 = keys and values only                                */
+    int32_t num_kv_heads;
+    int32_t head_dim;
+    int32_t rot_dim;        /* channels that are rotated, from channel 0               */
+    int32_t max_positions;  /* rows of the table                                       */
+    int32_t flags;          /* KVQ_ROPE_INTERLEAVED or 0                               */
+    int64_t q_stride;       /* elements between tokens; 0 = packed (heads * head_dim)  */
+    int64_t k_stride;
+    int64_t v_stride;
+} kvq_rope_params;
+
+int kv_append_rope_e4m3(const void *q, const void *k_new, const void *v_new, const int32_t *positions, const float *table,
+                        const int32_t *slot_mapping, void *q_out, uint8_t *k_cache, uint8_t *v_cache, int64_t num_pages,
+                        float k_scale, float v_scale, const kvq_rope_params *p, int32_t *err_flag, void *stream);
+int kv_append_rope_fp16(const void *q, const void *k_new, const void *v_new, const int32_t *positions, const float *table,
+                        const int32_t *slot_mapping, void *q_out, void *k_cache, void *v_cache, int64_t num_pages,
+                        const kvq_rope_params *p, int32_t *err_flag, void *stream);
+int kv_append_rope_e2m1(const void *q, const void *k_new, const void *v_new, const int32_t *positions, const float *table,
+                        const int32_t *slot_mapping, void *q_out, uint8_t *k_cache, uint8_t *v_cache, int64_t num_pages,
+                        float k_scale, float v_scale, const kvq_rope_params *p, int32_t *err_flag, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The 4-bit cache.  A channel of K or V is held as an E2M1 code (0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6 and their negatives), each block of 16 channels of a token
+ * with an E4M3 scale b, each layer with a calibrated scale S:
+ *     value = E2M1(code) * b * S
+ * 4.5 bits a channel: 9/16 of the E4M3 cache's bytes.  head_dim 64 or 128.
+ * A pool is uint8 [num_pages][num_kv_heads][9 * head_dim / 4]; a page of one
+ * kv head is its 4 tokens' codes, head_dim / 2 bytes each (channel 2 i in the
+ * low nibble of byte i), then the scales, [head_dim / 16 blocks][4 tokens].
+ *
+ * Quantiser, per block x[0..15] (every quotient and product one binary32
+ * operation, round to nearest even):
+ *     b    = E4M3(max |x| / (6 S))      saturating at 448
+ *     code = E2M1(x * (1 / (b S)))      to nearest even, saturating at 6;
+ *                                       0 where b = 0
+ * A NaN makes its block's scale NaN, and so the block.
+ * kvq_scale_from_amax_e2m1: host helper, amax / 2688 (2688 = 6 * 448, the
+ *   largest value a block holds in units of S), or 0 as kvq_scale_from_amax.
+ * Scales below 2^-100 or above 2^100 are refused too (KVQ_ERR_BAD_SCALE).
+ */
+float kvq_scale_from_amax_e2m1(float amax);
+
+/* Quantise-on-append into E2M1 pools; arguments as for kv_append_e4m3.  Slots
+ * >= 0 are distinct: of two tokens in one slot, neither is kept whole. */
+int kv_append_e2m1(const void *k_new, const void *v_new, const int32_t *slot_mapping, int32_t num_tokens,
+                   int32_t num_kv_heads, int32_t head_dim, uint8_t *k_cache, uint8_t *v_cache, int64_t num_pages,
+                   float k_scale, float v_scale, int32_t *err_flag, void *stream);
+
+/* Read-back: k_out[t][g][:] and v_out[t][g][:] = the values held at slots[t],
+ * rounded to fp16; zeros for a negative slot, and for one beyond the pool,
+ * which sets KVQ_DEV_BAD_SLOT.  For programs that move cached rows elsewhere
+ * or attend them with kernels of their own.
+ *   slots : device int32 [num_tokens];  k_out, v_out : device fp16
+ *   [num_tokens][num_kv_heads][head_dim], 16-B aligned */
+int kv_gather_e2m1(const uint8_t *k_cache, const uint8_t *v_cache, int64_t num_pages, const int32_t *slots,
+                   int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim, float k_scale, float v_scale, void *k_out,
+                   void *v_out, int32_t *err_flag, void *stream);
+
+/* Decode / verify attention over E2M1 pools: paged_decode_attn_e4m3 and its
+ * _partial form with these pools, the same parameters, workspace, masks,
+ * top-k lists and errors.  Of the flags only KVQ_ATTN_STRICT_ORDER applies;
+ * the others return KVQ_ERR_UNSUPPORTED.  kvq_lse_combine merges the
+ * partials.  Two launches: attention, combine. */
+int paged_decode_attn_e2m1(const void *q, const uint8_t *k_cache, const uint8_t *v_cache, int64_t num_pages,
+                           const int32_t *block_tables, const int32_t *context_lens, float k_scale, float v_scale,
+                           const int32_t *topk_idx, const int32_t *topk_lens, float *workspace, size_t workspace_bytes,
+                           void *out, const kvq_attn_params *p, int32_t *err_flag, void *stream);
+int paged_decode_attn_e2m1_partial(const void *q, const uint8_t *k_cache, const uint8_t *v_cache, int64_t num_pages,
+                                   const int32_t *block_tables, const int32_t *context_lens, float k_scale, float v_scale,
+                                   const int32_t *topk_idx, const int32_t *topk_lens, float *workspace,
+                                   size_t workspace_bytes, const kvq_attn_params *p, int32_t *err_flag, void *stream);
+
+/* Chunked-prefill attention over E2M1 pools: paged_prefill_attn_e4m3 with
+ * these pools (code times block scale is exact in the fp16 tiles). */
+int paged_prefill_attn_e2m1(const void *q, const uint8_t *k_cache, const uint8_t *v_cache, int64_t num_pages,
+                            const int32_t *block_tables, const int32_t *context_lens, const int32_t *q_start,
+                            float k_scale, float v_scale, void *workspace, size_t workspace_bytes, void *out,
                             const kvq_prefill_params *p, int32_t *err_flag, void *stream);
 
 /* ------------------------------------------------------------------------
