@@ -34,48 +34,200 @@ constexpr int kQWarps = 4;
 constexpr int kQThreads = 32 * kQWarps;
 constexpr int kUnitTiles = 2;                   // 16-token tiles a warp takes at once
 constexpr int kUnitPages = 4 * kUnitTiles;
+static_assert(kUnitPages == 8, "a unit's 32 tokens have a lane each");
 
 template <int D>
-struct Frag {
-    static constexpr int KW = D / 32;   // words of 8 codes per K row and lane
-    static constexpr int KB = D / 64;   // blocks of 16 channels they span (scale words)
-    static constexpr int VW = D / 64;   // words of 8 codes per V token and lane
-    uint32_t k[2][KW];
-    uint32_t ks[KB];                    // a block's scales of the page's four tokens
-    uint32_t v[4][VW];
-    uint32_t vs;                        // this lane's block's scales of the page's four tokens
+struct KFrag {
+    static constexpr int KW = D / 32;   // words of 8 codes per row and lane
+    static constexpr int KB = D / 64;   // blocks of 16 channels they span
+    uint32_t x[2][KW];
+    uint32_t s[KB];                     // a block's scales of the page's four tokens
+};
+
+template <int D>
+struct VFrag {
+    static constexpr int VW = D / 64;   // words of 8 codes per token and lane
+    uint32_t x[4][VW];
+    uint32_t s;                         // this lane's block's scales of the page's four tokens
 };
 
 template <int W>
 __device__ __forceinline__ void load_words(uint32_t (&x)[W], const uint8_t *p)
 {
     static_assert(W == 1 || W == 2 || W == 4, "4, 8 or 16 bytes");
-    if (W == 4) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+    if constexpr (W == 4) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(p);
         x[0] = u.x;
-        x[W > 1 ? 1 : 0] = u.y;
-        x[W > 2 ? 2 : 0] = u.z;
-        x[W > 3 ? 3 : 0] = u.w;
-    } else if (W == 2) {
-        const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
+        x[1] = u.y;
+        x[2] = u.z;
+        x[3] = u.w;
+    } else if constexpr (W == 2) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(p);
         x[0] = u.x;
-        x[W > 1 ? 1 : 0] = u.y;
+        x[1] = u.y;
     } else {
-        x[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+        x[0] = *reinterpret_cast<const uint32_t *>(p);
     }
 }
 
-template <int W>
-__device__ __forceinline__ void zero_words(uint32_t (&x)[W])
+// bits 0..3 -> bytes of all ones
+__device__ __forceinline__ uint32_t byte_mask(uint32_t bits)
 {
-#pragma unroll
-    for (int i = 0; i < W; ++i) x[i] = 0u;
+    return ((bits * 0x00204081u) & 0x01010101u) * 0xFFu;
 }
 
 }  // namespace
 
+// A warp's ring of units in shared memory.  A lane copies the bytes of its own
+// fragments (cp.async) and reads them back itself, so neither needs a barrier.
+// Fields of a tile, each [32 lanes][bytes]: K row 0, K row 1, K scales, V codes
+// of tokens 0..3, V scale.
+template <int D>
+struct Ring {
+    static constexpr int kK = D / 8, kKS = D / 16, kV = D / 16, kVS = 4;   // bytes per lane
+    static constexpr int kOffKS = 2 * 32 * kK, kOffV = kOffKS + 32 * kKS, kOffVS = kOffV + 4 * 32 * kV;
+    static constexpr int kTile = kOffVS + 32 * kVS;
+    static constexpr int kUnit = kUnitTiles * kTile;
+    static constexpr int kUnits = 2;
+    static constexpr int kBytes = kUnits * kUnit;
+};
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const uint8_t *src)
+{
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <int PENDING>
+__device__ __forceinline__ void copy_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
+// One tile's S^T = K Q^T
+template <int D, int NT>
+__device__ __forceinline__ void scores(const KFrag<D> &f, uint32_t ks_sel, const uint32_t (&qf)[NT][D / 16][2],
+                                       float (&sc)[NT][kUnitTiles][4], int k)
+{
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[j][k][e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < KFrag<D>::KW; ++w) {
+        // the block's scale of this lane's two rows, in both halves
+        const uint32_t sb = __byte_perm(f.s[w / 2], 0u, ks_sel);
+        const uint32_t s0 = cvt_lo(sb), s1 = cvt_hi(sb);
+        const uint32_t x0 = f.x[0][w], x1 = f.x[1][w];
+        const uint32_t lo[4] = {hmul2(e2m1_pair<0>(x0), s0), hmul2(e2m1_pair<0>(x1), s1),
+                                hmul2(e2m1_pair<1>(x0), s0), hmul2(e2m1_pair<1>(x1), s1)};
+        const uint32_t hi[4] = {hmul2(e2m1_pair<2>(x0), s0), hmul2(e2m1_pair<2>(x1), s1),
+                                hmul2(e2m1_pair<3>(x0), s0), hmul2(e2m1_pair<3>(x1), s1)};
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            mma_16816(sc[j][k], lo, qf[j][2 * w][0], qf[j][2 * w][1]);
+            mma_16816(sc[j][k], hi, qf[j][2 * w + 1][0], qf[j][2 * w + 1][1]);
+        }
+    }
+}
+
+// One tile's O^T += V^T P^T
+template <int D, int NT>
+__device__ __forceinline__ void weigh(const VFrag<D> &f, const uint32_t (&pf)[NT][kUnitTiles][2], float (&o)[NT][D / 16][4], int k)
+{
+    const uint32_t s01 = cvt_lo(f.s), s23 = cvt_hi(f.s);
+#pragma unroll
+    for (int w = 0; w < VFrag<D>::VW; ++w) {
+        // channels 8w + 2y (z0, y0) and 8w + 2y + 1 (z1, y1) of byte y, two tokens a byte
+        constexpr uint32_t M = 0x0F0F0F0Fu;
+        const uint32_t z0 = (f.x[0][w] & M) | ((f.x[1][w] << 4) & ~M);
+        const uint32_t z1 = ((f.x[0][w] >> 4) & M) | (f.x[1][w] & ~M);
+        const uint32_t y0 = (f.x[2][w] & M) | ((f.x[3][w] << 4) & ~M);
+        const uint32_t y1 = ((f.x[2][w] >> 4) & M) | (f.x[3][w] & ~M);
+        const uint32_t af[4][4] = {
+            {hmul2(e2m1_pair<0>(z0), s01), hmul2(e2m1_pair<0>(z1), s01), hmul2(e2m1_pair<0>(y0), s23), hmul2(e2m1_pair<0>(y1), s23)},
+            {hmul2(e2m1_pair<1>(z0), s01), hmul2(e2m1_pair<1>(z1), s01), hmul2(e2m1_pair<1>(y0), s23), hmul2(e2m1_pair<1>(y1), s23)},
+            {hmul2(e2m1_pair<2>(z0), s01), hmul2(e2m1_pair<2>(z1), s01), hmul2(e2m1_pair<2>(y0), s23), hmul2(e2m1_pair<2>(y1), s23)},
+            {hmul2(e2m1_pair<3>(z0), s01), hmul2(e2m1_pair<3>(z1), s01), hmul2(e2m1_pair<3>(y0), s23), hmul2(e2m1_pair<3>(y1), s23)}};
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) mma_16816(o[j][4 * w + y], af[y], pf[j][k][0], pf[j][k][1]);
+    }
+}
+
+// Softmax of a unit: scores to P (fp16, as mma B fragments), sums, and the rescale of O.
+template <int D, int NT>
+__device__ __forceinline__ void softmax_unit(const float (&sc)[NT][kUnitTiles][4], float qk, float (&ref)[NT][2],
+                                             float (&l_run)[NT][2], float (&o)[NT][D / 16][4],
+                                             uint32_t (&pf)[NT][kUnitTiles][2])
+{
+    // A row's reference moves only when a score rises more than 2^8 above
+    // it (P and its sum stay below 2^8 times their number), so most units
+    // need no maximum over the lanes and no rescale: one vote.
+    bool above = false;
+    float mx[NT][2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            float m = fmaxf(sc[j][0][c], sc[j][0][c + 2]);
+#pragma unroll
+            for (int k = 1; k < kUnitTiles; ++k) m = fmax3(m, sc[j][k][c], sc[j][k][c + 2]);
+            mx[j][c] = m * qk;
+            above |= mx[j][c] > ref[j][c] + 8.f;
+        }
+    if (__any_sync(kFull, above)) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            float corr[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float m = mx[j][c];
+                m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
+                m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
+                m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
+                const bool move = m > ref[j][c] + 8.f;   // the same on the 8 lanes of a row
+                corr[c] = !move ? 1.f : ref[j][c] == -INFINITY ? 0.f : fast_exp2(ref[j][c] - m);
+                if (move) ref[j][c] = m;
+                l_run[j][c] *= corr[c];
+            }
+#pragma unroll
+            for (int pv = 0; pv < D / 16; ++pv) {
+                o[j][pv][0] *= corr[0];
+                o[j][pv][2] *= corr[0];
+                o[j][pv][1] *= corr[1];
+                o[j][pv][3] *= corr[1];
+            }
+        }
+    }
+    const float2 qk2 = make_float2(qk, qk);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        // a row that has seen nothing yet: every score is -inf, P = 0
+        const float2 nref = make_float2(ref[j][0] == -INFINITY ? 0.f : -ref[j][0], ref[j][1] == -INFINITY ? 0.f : -ref[j][1]);
+        float2 sum = make_float2(l_run[j][0], l_run[j][1]);
+#pragma unroll
+        for (int k = 0; k < kUnitTiles; ++k)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float2 z = ffma2(make_float2(sc[j][k][2 * r], sc[j][k][2 * r + 1]), qk2, nref);
+                const float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
+                sum = fadd2(sum, p);
+                pf[j][k][r] = movmatrix_trans(pack_half2(p.x, p.y));
+            }
+        l_run[j][0] = sum.x;
+        l_run[j][1] = sum.y;
+    }
+}
+
 // NT n-tiles of 8 query rows per warp; RW warps share the same tokens and split
-// the query rows, the 4 / RW groups of warps split the tokens.
+// the query rows, the kQWarps / RW groups of warps split the tokens.
 template <int D, int NT, int RW>
 __global__ void __launch_bounds__(kQThreads, NT == 1 ? 4 : 3) attn_e2m1_kernel(const AttnArgs a)
 {
@@ -84,27 +236,94 @@ __global__ void __launch_bounds__(kQThreads, NT == 1 ? 4 : 3) attn_e2m1_kernel(c
     constexpr int kRowF = D + 4;                     // m, l, two unused, o[D]
     constexpr int PB = e2m1_page_bytes(D), SO = e2m1_scale_off(D);
     constexpr int CPL = D / 4;                       // K channels per lane
-    using F = Frag<D>;
+    using KF = KFrag<D>;
+    using VF = VFrag<D>;
+    using R = Ring<D>;
     extern __shared__ __align__(16) uint8_t smem[];
 
     const int s = blockIdx.x, g = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gid = lane >> 2, t = lane & 3;
     const int rw = warp % RW, tw = warp / RW;
-    grid_dependency_wait();
+    // Without a top-k list, block tables, lengths and the pages of positions
+    // below L - q_len may be read before the preceding kernel (the step's
+    // append) has finished; everything else waits for it.
+    const bool early = a.early_pages && a.topk_idx == nullptr;
+    if (!early) grid_dependency_wait();
     launch_dependents();
     const SeqPick pick = seq_identity(a, blockIdx.z);
     const int b = pick.b;
     const SplitRange sr = split_range(a, s, b, pick.L, pick.topk_len);
     const int L = sr.L, item0 = sr.item0, item1 = sr.item1;
-    const bool topk = sr.topk;
+
+    // this lane's places inside a page
+    const int page_stride = a.num_kv_heads * PB;   // at most 65535 * 288
+    const uint8_t *kpool = static_cast<const uint8_t *>(a.k_cache) + (int64_t)g * PB;
+    const uint8_t *vpool = static_cast<const uint8_t *>(a.v_cache) + (int64_t)g * PB;
+    const int k_code = t * (CPL / 2), k_scale = SO + t * (4 * KF::KB);
+    const int v_code = gid * (D / 16), v_scale = SO + 4 * (gid * D / 128);
+    const uint32_t ks_sel = (gid & 1) ? 0x3311u : 0x2200u;   // scale bytes (row, row, row + 8, row + 8)
+
+    // --- dense: a unit is 8 pages; lane l (mod 8) holds page l's number (-1: none) ---
+    const int step = TW * kUnitPages;
+    int u0 = item0 + tw * kUnitPages;
+    auto raw_page = [&](int u) {
+        const int it = u + (lane & (kUnitPages - 1));
+        return it < item1 ? __ldg(sr.bt_row + it) : -1;
+    };
+    auto checked = [&](int phys, int u) {
+        if (phys >= 0 && (int64_t)phys < a.num_pages) return phys;
+        if (u + (lane & (kUnitPages - 1)) < item1 && rw == 0 && lane < kUnitPages) report(a.err_flag, KVQ_DEV_BAD_PAGE);
+        return -1;
+    };
+    uint8_t *ring = smem + warp * R::kBytes;
+    const uint32_t ring_s = smem_u32(ring);
+    const uint8_t *k_rows = kpool + k_code + (gid & 1) * (D / 2), *k_scales = kpool + k_scale;
+    const uint8_t *v_rows = vpool + v_code, *v_scales = vpool + v_scale;
+    // Copies of a unit into ring slot `slot`.  Missing pages are read from page 0 and masked.
+    auto fetch = [&](int phys, int slot) {
+        const int page = max(phys, 0);
+#pragma unroll
+        for (int k = 0; k < kUnitTiles; ++k) {
+            const uint32_t dst = ring_s + slot * R::kUnit + k * R::kTile;
+            const int64_t kp = (int64_t)__shfl_sync(kFull, page, 4 * k + (gid >> 1)) * page_stride;
+            const int64_t vp = (int64_t)__shfl_sync(kFull, page, 4 * k + t) * page_stride;
+            copy_async<R::kK>(dst + lane * R::kK, k_rows + kp);
+            copy_async<R::kK>(dst + 32 * R::kK + lane * R::kK, k_rows + kp + D);
+            copy_async<R::kKS>(dst + R::kOffKS + lane * R::kKS, k_scales + kp);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                copy_async<R::kV>(dst + R::kOffV + j * 32 * R::kV + lane * R::kV, v_rows + vp + j * (D / 2));
+            copy_async<R::kVS>(dst + R::kOffVS + lane * R::kVS, v_scales + vp);
+        }
+    };
+    int pg[R::kUnits + 1];                 // pages of the units in flight and of the one after
+    bool waited = !early;
+    if (!sr.topk) {
+#pragma unroll
+        for (int d = 0; d <= R::kUnits; ++d) pg[d] = raw_page(u0 + d * step);
+#pragma unroll
+        for (int d = 0; d < R::kUnits; ++d) {
+            const int u = u0 + d * step;
+            if (u < item1) {
+                if (!waited && u + kUnitPages > max(L - a.q_len, 0) / 4) {
+                    grid_dependency_wait();
+                    waited = true;
+                }
+                pg[d] = checked(pg[d], u);
+                fetch(pg[d], d);
+            }
+            copy_commit();
+        }
+    }
+    if (!waited) grid_dependency_wait();
     if (threadIdx.x == 0) {
         if (!sr.len_ok) report(a.err_flag, KVQ_DEV_BAD_LEN);
         if (sr.len_ok && pick.topk_len > a.max_topk) report(a.err_flag, KVQ_DEV_BAD_TOPK);
     }
 
     float o[NT][D / 16][4];
-    float m_run[NT][2], l_run[NT][2];
+    float ref[NT][2], l_run[NT][2];       // log2-domain reference of a row, sum of its 2^(s - ref)
     uint32_t qf[NT][D / 16][2];
     int lim[NT][2];
 #pragma unroll
@@ -113,8 +332,8 @@ __global__ void __launch_bounds__(kQThreads, NT == 1 ? 4 : 3) attn_e2m1_kernel(c
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             const int r = (rw * NT + j) * 8 + 2 * t + c;
-            lim[j][c] = (r < a.rows) ? L - a.q_len + r / a.group : 0x7FFFFFFF;
-            m_run[j][c] = -INFINITY;
+            lim[j][c] = (r < a.rows) ? L - a.q_len + r / a.group : 0x7FFFFFFE;
+            ref[j][c] = -INFINITY;
             l_run[j][c] = 0.f;
         }
 #pragma unroll
@@ -135,214 +354,134 @@ __global__ void __launch_bounds__(kQThreads, NT == 1 ? 4 : 3) attn_e2m1_kernel(c
             }
         }
     }
-    const uint8_t *kpool = static_cast<const uint8_t *>(a.k_cache);
-    const uint8_t *vpool = static_cast<const uint8_t *>(a.v_cache);
-    const int first_masked = L - a.q_len + 1;        // positions from here on are masked for some row
-    const uint32_t ks_sel = (gid & 1) ? 0x3311u : 0x2200u;   // scale bytes (row, row, row + 8, row + 8)
+    const float qk = a.qk_scale_log2;
+    float sc[NT][kUnitTiles][4];
+    uint32_t pf[NT][kUnitTiles][2];
+    constexpr int kNoToken = 0x7FFFFFFF;   // a position beyond every row's limit
 
-    const int ipu = topk ? 4 * kUnitPages : kUnitPages;   // items per unit: pages or list entries
-    const int32_t *list = topk ? a.topk_idx + ((int64_t)b * a.num_kv_heads + g) * a.max_topk : nullptr;
-    for (int u0 = item0 + tw * ipu; u0 < item1; u0 += TW * ipu) {
-        F f[kUnitTiles];
-        int kpos[kUnitTiles][2];          // positions of this lane's K rows, -1 = no token
-        uint32_t vlive[kUnitTiles];       // 0xFF in byte j: token j of this lane's V page holds a token
-        bool need_mask;
-        if (!topk) {
-            const int it = u0 + (lane & (kUnitPages - 1));
-            int phys = it < item1 ? __ldg(sr.bt_row + it) : -1;
-            const bool bad = it < item1 && (phys < 0 || (int64_t)phys >= a.num_pages);
-            if (bad) phys = -1;
-            if (bad && rw == 0 && lane < kUnitPages) report(a.err_flag, KVQ_DEV_BAD_PAGE);
-            need_mask = __any_sync(kFull, phys < 0) || (u0 + kUnitPages) * 4 > first_masked;
+    if (!sr.topk) {
+        const int first_masked = L - a.q_len + 1;        // positions from here on are masked for some row
+        int slot = 0;
+        for (; u0 < item1; u0 += step) {
+            const int ahead = raw_page(u0 + (R::kUnits + 1) * step);
+            copy_wait<R::kUnits - 1>();
+            const uint8_t *un = ring + slot * R::kUnit;
 #pragma unroll
             for (int k = 0; k < kUnitTiles; ++k) {
-                const int kp = __shfl_sync(kFull, phys, 4 * k + (gid >> 1));
-                const int vp = __shfl_sync(kFull, phys, 4 * k + t);
-                const int kpos0 = (u0 + 4 * k + (gid >> 1)) * 4 + (gid & 1);
-                kpos[k][0] = kp >= 0 ? kpos0 : -1;
-                kpos[k][1] = kp >= 0 ? kpos0 + 2 : -1;
-                const int vleft = vp >= 0 ? L - (u0 + 4 * k + t) * 4 : 0;   // tokens of the page inside the context
-                vlive[k] = vleft >= 4 ? 0xFFFFFFFFu : vleft <= 0 ? 0u : (1u << (8 * vleft)) - 1u;
-                zero_words(f[k].k[0]);
-                zero_words(f[k].k[1]);
-                zero_words(f[k].ks);
-                if (kp >= 0) {
-                    const uint8_t *pg = kpool + ((int64_t)kp * a.num_kv_heads + g) * PB;
-                    load_words(f[k].k[0], pg + (gid & 1) * (D / 2) + t * (CPL / 2));
-                    load_words(f[k].k[1], pg + (2 + (gid & 1)) * (D / 2) + t * (CPL / 2));
-                    load_words(f[k].ks, pg + SO + t * (4 * F::KB));
-                }
-                f[k].vs = 0u;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) zero_words(f[k].v[j]);
-                if (vp >= 0) {
-                    const uint8_t *pg = vpool + ((int64_t)vp * a.num_kv_heads + g) * PB;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) load_words(f[k].v[j], pg + j * (D / 2) + gid * (D / 16));
-                    f[k].vs = __ldg(reinterpret_cast<const uint32_t *>(pg + SO + 4 * (gid * D / 128)));
-                }
+                const uint8_t *tl = un + k * R::kTile;
+                KF f;
+                load_words(f.x[0], tl + lane * R::kK);
+                load_words(f.x[1], tl + 32 * R::kK + lane * R::kK);
+                load_words(f.s, tl + R::kOffKS + lane * R::kKS);
+                scores<D, NT>(f, ks_sel, qf, sc, k);
             }
-        } else {
-            // entry 16 k + 4 p + j of the unit is token j of page slot p of tile k
-            const int it = u0 + lane;
-            const bool exists = it < item1;
-            int idx = exists ? __ldg(list + it) : -1;
-            const bool idx_ok = idx >= 0 && idx < L;
-            if (exists && !idx_ok && rw == 0) report(a.err_flag, KVQ_DEV_BAD_TOPK);
-            int phys = idx_ok ? __ldg(sr.bt_row + (idx >> 2)) : -1;
-            if (idx_ok && (phys < 0 || (int64_t)phys >= a.num_pages)) {
-                if (rw == 0) report(a.err_flag, KVQ_DEV_BAD_PAGE);
-                phys = -1;
-            }
-            if (phys < 0) idx = -1;
-            need_mask = true;
+            const unsigned paged = __ballot_sync(kFull, pg[0] >= 0);   // bits 0..7 (and their copies): pages
+            uint32_t vmask[kUnitTiles];
 #pragma unroll
-            for (int k = 0; k < kUnitTiles; ++k) {
-                zero_words(f[k].ks);
+            for (int k = 0; k < kUnitTiles; ++k) vmask[k] = 0xFFFFFFFFu;
+            if (paged != kFull || u0 + kUnitPages > first_masked / 4) {
+                // Slots without a token may hold any bits: their scores are replaced (whatever they
+                // are), and their V scales zeroed, since a NaN scale times a probability of 0 is NaN.
+                const unsigned live = __ballot_sync(kFull, ((paged >> (lane >> 2)) & 1u) && u0 * 4 + lane < L);
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int e = 16 * k + 4 * (gid >> 1) + (gid & 1) + 2 * r;
-                    const int kp = __shfl_sync(kFull, phys, e), ki = __shfl_sync(kFull, idx, e);
-                    kpos[k][r] = ki;
-                    zero_words(f[k].k[r]);
-                    if (ki >= 0) {
-                        const uint8_t *pg = kpool + ((int64_t)kp * a.num_kv_heads + g) * PB;
-                        load_words(f[k].k[r], pg + (ki & 3) * (D / 2) + t * (CPL / 2));
+                for (int k = 0; k < kUnitTiles; ++k) {
 #pragma unroll
-                        for (int w = 0; w < F::KB; ++w)
-                            f[k].ks[w] |= (uint32_t)__ldg(pg + SO + 4 * (t * F::KB + w) + (ki & 3))
-                                          << (8 * ((gid & 1) + 2 * r));
+                    for (int r = 0; r < 2; ++r) {
+                        const int e = 16 * k + 4 * (gid >> 1) + (gid & 1) + 2 * r;
+                        const int pos = ((live >> e) & 1u) ? u0 * 4 + e : kNoToken;
+#pragma unroll
+                        for (int j = 0; j < NT; ++j)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+                                if (pos > lim[j][c]) sc[j][k][2 * r + c] = -INFINITY;
                     }
+                    vmask[k] = byte_mask((live >> (16 * k + 4 * t)) & 15u);
                 }
-                f[k].vs = 0u;
-                vlive[k] = 0xFFFFFFFFu;
+            }
+            softmax_unit<D, NT>(sc, qk, ref, l_run, o, pf);
+#pragma unroll
+            for (int k = 0; k < kUnitTiles; ++k) {
+                const uint8_t *tl = un + k * R::kTile;
+                VF f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) load_words(f.x[j], tl + R::kOffV + j * 32 * R::kV + lane * R::kV);
+                f.s = *reinterpret_cast<const uint32_t *>(tl + R::kOffVS + lane * R::kVS) & vmask[k];
+                weigh<D, NT>(f, pf, o, k);
+            }
+            // this slot has been read (by this lane alone): the unit after those in flight
+            const int u = u0 + R::kUnits * step;
+            pg[R::kUnits] = checked(pg[R::kUnits], u);
+            if (u < item1) fetch(pg[R::kUnits], slot);
+            copy_commit();
+            slot = slot + 1 == R::kUnits ? 0 : slot + 1;
+#pragma unroll
+            for (int d = 0; d < R::kUnits; ++d) pg[d] = pg[d + 1];
+            pg[R::kUnits] = ahead;
+        }
+    } else {
+        // --- top-k: a unit is 32 list entries; entry 16 k + 4 p + j is token j of page slot p of
+        // tile k; lane l holds entry l's position (-1: none) and page ---
+        const int32_t *list = a.topk_idx + ((int64_t)b * a.num_kv_heads + g) * a.max_topk;
+        for (int e0 = item0 + tw * 32; e0 < item1; e0 += TW * 32) {
+            int pos = e0 + lane < item1 ? __ldg(list + e0 + lane) : -1;
+            int phys = 0;
+            if (e0 + lane < item1 && (pos < 0 || pos >= L)) {
+                if (rw == 0) report(a.err_flag, KVQ_DEV_BAD_TOPK);
+                pos = -1;
+            }
+            if (pos >= 0) {
+                phys = __ldg(sr.bt_row + (pos >> 2));
+                if (phys < 0 || (int64_t)phys >= a.num_pages) {
+                    if (rw == 0) report(a.err_flag, KVQ_DEV_BAD_PAGE);
+                    pos = -1;
+                    phys = 0;
+                }
+            }
+            const unsigned live = __ballot_sync(kFull, pos >= 0);
+            VF vf[kUnitTiles];
+#pragma unroll
+            for (int k = 0; k < kUnitTiles; ++k) {
+                vf[k].s = 0u;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int e = 16 * k + 4 * t + j;
-                    const int vp = __shfl_sync(kFull, phys, e), vi = __shfl_sync(kFull, idx, e);
-                    zero_words(f[k].v[j]);
-                    if (vi >= 0) {
-                        const uint8_t *pg = vpool + ((int64_t)vp * a.num_kv_heads + g) * PB;
-                        load_words(f[k].v[j], pg + (vi & 3) * (D / 2) + gid * (D / 16));
-                        f[k].vs |= (uint32_t)__ldg(pg + SO + 4 * (gid * D / 128) + (vi & 3)) << (8 * j);
-                    }
+                    const int at = __shfl_sync(kFull, pos, e) & 3;
+                    const uint8_t *row = vpool + (int64_t)__shfl_sync(kFull, phys, e) * page_stride;
+                    load_words(vf[k].x[j], row + v_code + at * (D / 2));
+                    vf[k].s |= (uint32_t)row[v_scale + at] << (8 * j);
                 }
+                vf[k].s &= byte_mask((live >> (16 * k + 4 * t)) & 15u);
             }
-        }
-
-        // ---- S^T = K Q^T ----
-        float sc[NT][kUnitTiles][4];
-#pragma unroll
-        for (int k = 0; k < kUnitTiles; ++k) {
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sc[j][k][e] = 0.f;
-#pragma unroll
-            for (int w = 0; w < F::KW; ++w) {
-                // the block's scale of this lane's two rows, in both halves
-                const uint32_t sb = __byte_perm(f[k].ks[w / 2], 0u, ks_sel);
-                const uint32_t s0 = cvt_lo(sb), s1 = cvt_hi(sb);
-                const uint32_t x0 = f[k].k[0][w], x1 = f[k].k[1][w];
-                const uint32_t lo[4] = {hmul2(e2m1_pair<0>(x0), s0), hmul2(e2m1_pair<0>(x1), s1),
-                                        hmul2(e2m1_pair<1>(x0), s0), hmul2(e2m1_pair<1>(x1), s1)};
-                const uint32_t hi[4] = {hmul2(e2m1_pair<2>(x0), s0), hmul2(e2m1_pair<2>(x1), s1),
-                                        hmul2(e2m1_pair<3>(x0), s0), hmul2(e2m1_pair<3>(x1), s1)};
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    mma_16816(sc[j][k], lo, qf[j][2 * w][0], qf[j][2 * w][1]);
-                    mma_16816(sc[j][k], hi, qf[j][2 * w + 1][0], qf[j][2 * w + 1][1]);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sc[j][k][e] *= a.qk_scale_log2;
-        }
-        if (need_mask) {
-            // Slots without a token may hold any bits: their scores are replaced (whatever they
-            // are), and their V scales zeroed, since a NaN scale times a probability of 0 is NaN.
 #pragma unroll
             for (int k = 0; k < kUnitTiles; ++k) {
+                KF f;
+#pragma unroll
+                for (int w = 0; w < KF::KB; ++w) f.s[w] = 0u;
+                int row_pos[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int e = 16 * k + 4 * (gid >> 1) + (gid & 1) + 2 * r;
+                    const int p = __shfl_sync(kFull, pos, e), at = p & 3;
+                    const uint8_t *row = kpool + (int64_t)__shfl_sync(kFull, phys, e) * page_stride;
+                    row_pos[r] = p >= 0 ? p : kNoToken;
+                    load_words(f.x[r], row + k_code + at * (D / 2));
+#pragma unroll
+                    for (int w = 0; w < KF::KB; ++w) f.s[w] |= (uint32_t)row[k_scale + 4 * w + at] << (8 * ((gid & 1) + 2 * r));
+                }
+                scores<D, NT>(f, ks_sel, qf, sc, k);
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int pos = kpos[k][e >> 1];
-                        if (!(pos >= 0 && pos <= lim[j][e & 1])) sc[j][k][e] = -INFINITY;
-                    }
-                f[k].vs &= vlive[k];
+                    for (int e = 0; e < 4; ++e)
+                        if (row_pos[e >> 1] > lim[j][e & 1]) sc[j][k][e] = -INFINITY;
             }
-        }
-        // ---- online softmax (a column's rows lie on the 8 lanes that share t) ----
-        float corr[NT][2];
-        bool raised = false;
+            softmax_unit<D, NT>(sc, qk, ref, l_run, o, pf);
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                float mx = fmaxf(sc[j][0][c], sc[j][0][c + 2]);
-#pragma unroll
-                for (int k = 1; k < kUnitTiles; ++k) mx = fmaxf(mx, fmaxf(sc[j][k][c], sc[j][k][c + 2]));
-                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
-                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
-                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
-                const float m_new = fmaxf(m_run[j][c], mx);
-                const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
-                const bool up = m_new != m_run[j][c];
-                corr[j][c] = up ? fast_exp2(m_run[j][c] - m_use) : 1.f;
-                raised |= up;
-                m_run[j][c] = m_new;
-                float lsum = l_run[j][c] * corr[j][c];
-#pragma unroll
-                for (int k = 0; k < kUnitTiles; ++k) {
-                    sc[j][k][c] = fast_exp2(sc[j][k][c] - m_use);
-                    sc[j][k][c + 2] = fast_exp2(sc[j][k][c + 2] - m_use);
-                    lsum += sc[j][k][c] + sc[j][k][c + 2];
-                }
-                l_run[j][c] = lsum;
-            }
-        if (__any_sync(kFull, raised)) {
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int pv = 0; pv < D / 16; ++pv) {
-                    o[j][pv][0] *= corr[j][0];
-                    o[j][pv][2] *= corr[j][0];
-                    o[j][pv][1] *= corr[j][1];
-                    o[j][pv][3] *= corr[j][1];
-                }
-        }
-        // ---- O^T += V^T P^T ----
-#pragma unroll
-        for (int k = 0; k < kUnitTiles; ++k) {
-            uint32_t pf[NT][2];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                pf[j][0] = movmatrix_trans(pack_half2(sc[j][k][0], sc[j][k][1]));
-                pf[j][1] = movmatrix_trans(pack_half2(sc[j][k][2], sc[j][k][3]));
-            }
-            const uint32_t s01 = cvt_lo(f[k].vs), s23 = cvt_hi(f[k].vs);
-#pragma unroll
-            for (int w = 0; w < F::VW; ++w) {
-                // channels 8w + 2y (z0) and 8w + 2y + 1 (z1) of byte y, two tokens a byte
-                constexpr uint32_t M = 0x0F0F0F0Fu;
-                const uint32_t z0 = (f[k].v[0][w] & M) | ((f[k].v[1][w] << 4) & ~M);
-                const uint32_t z1 = ((f[k].v[0][w] >> 4) & M) | (f[k].v[1][w] & ~M);
-                const uint32_t y0 = (f[k].v[2][w] & M) | ((f[k].v[3][w] << 4) & ~M);
-                const uint32_t y1 = ((f[k].v[2][w] >> 4) & M) | (f[k].v[3][w] & ~M);
-                const uint32_t af[4][4] = {
-                    {hmul2(e2m1_pair<0>(z0), s01), hmul2(e2m1_pair<0>(z1), s01), hmul2(e2m1_pair<0>(y0), s23), hmul2(e2m1_pair<0>(y1), s23)},
-                    {hmul2(e2m1_pair<1>(z0), s01), hmul2(e2m1_pair<1>(z1), s01), hmul2(e2m1_pair<1>(y0), s23), hmul2(e2m1_pair<1>(y1), s23)},
-                    {hmul2(e2m1_pair<2>(z0), s01), hmul2(e2m1_pair<2>(z1), s01), hmul2(e2m1_pair<2>(y0), s23), hmul2(e2m1_pair<2>(y1), s23)},
-                    {hmul2(e2m1_pair<3>(z0), s01), hmul2(e2m1_pair<3>(z1), s01), hmul2(e2m1_pair<3>(y0), s23), hmul2(e2m1_pair<3>(y1), s23)}};
-#pragma unroll
-                for (int y = 0; y < 4; ++y)
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) mma_16816(o[j][4 * w + y], af[y], pf[j][0], pf[j][1]);
-            }
+            for (int k = 0; k < kUnitTiles; ++k) weigh<D, NT>(vf[k], pf, o, k);
         }
     }
+    copy_wait<0>();     // the last groups are empty
+    __syncthreads();    // the merge reuses the rings
 
     // ---- the warps' results to shared memory, merged, to the workspace ----
     float *mbuf = reinterpret_cast<float *>(smem);       // [TW][kRowsPad][kRowF]
@@ -356,7 +495,7 @@ __global__ void __launch_bounds__(kQThreads, NT == 1 ? 4 : 3) attn_e2m1_kernel(c
             l += __shfl_xor_sync(kFull, l, 16);
             float *dst = mbuf + (tw * kRowsPad + (rw * NT + j) * 8 + 2 * t + c) * kRowF;
             if (gid == 0) {
-                dst[0] = m_run[j][c];
+                dst[0] = ref[j][c];
                 dst[1] = l;
             }
             // lane (gid, t): the D / 8 channels from gid D / 8 on, a pair per P V tile
@@ -404,7 +543,8 @@ __global__ void __launch_bounds__(kQThreads, NT == 1 ? 4 : 3) attn_e2m1_kernel(c
 template <int D, int NT, int RW>
 static cudaError_t launch_e2m1(const AttnArgs &a, cudaStream_t stream)
 {
-    constexpr int bytes = (kQWarps / RW) * RW * NT * 8 * (D + 4) * 4;
+    constexpr int merge = kQWarps * NT * 8 * (D + 4) * 4, ring = kQWarps * Ring<D>::kBytes;
+    constexpr int bytes = merge > ring ? merge : ring;
     static uint64_t configured = 0;   // one bit per device ordinal
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
