@@ -32,6 +32,8 @@ namespace {
 
 constexpr int kQWarps = 4;
 constexpr int kQThreads = 32 * kQWarps;
+// CTAs per SM, by registers: O takes D / 4 a thread and n-tile
+template <int NT> __host__ __device__ constexpr int ctas_per_sm() { return NT == 1 ? 4 : NT == 2 ? 3 : 2; }
 constexpr int kUnitTiles = 2;                   // 16-token tiles a warp takes at once
 constexpr int kUnitPages = 4 * kUnitTiles;
 static_assert(kUnitPages == 8, "a unit's 32 tokens have a lane each");
@@ -82,13 +84,13 @@ __device__ __forceinline__ uint32_t byte_mask(uint32_t bits)
 // fragments (cp.async) and reads them back itself, so neither needs a barrier.
 // Fields of a tile, each [32 lanes][bytes]: K row 0, K row 1, K scales, V codes
 // of tokens 0..3, V scale.
-template <int D>
+template <int D, int NT>
 struct Ring {
     static constexpr int kK = D / 8, kKS = D / 16, kV = D / 16, kVS = 4;   // bytes per lane
     static constexpr int kOffKS = 2 * 32 * kK, kOffV = kOffKS + 32 * kKS, kOffVS = kOffV + 4 * 32 * kV;
     static constexpr int kTile = kOffVS + 32 * kVS;
     static constexpr int kUnit = kUnitTiles * kTile;
-    static constexpr int kUnits = 2;
+    static constexpr int kUnits = NT <= 2 ? 2 : 3;
     static constexpr int kBytes = kUnits * kUnit;
 };
 
@@ -109,29 +111,63 @@ __device__ __forceinline__ void copy_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
 
-// One tile's S^T = K Q^T
+// The queries as mma B fragments: in registers for one n-tile, in shared memory
+// (in fragment order, [D / 32][RW * NT][32 lanes] of 16 bytes) for more.
+template <int D, int NT, int RW> __host__ __device__ constexpr int q_bytes() { return NT == 1 ? 0 : RW * NT * D * 16; }
+
 template <int D, int NT>
-__device__ __forceinline__ void scores(const KFrag<D> &f, uint32_t ks_sel, const uint32_t (&qf)[NT][D / 16][2],
-                                       float (&sc)[NT][kUnitTiles][4], int k)
+struct Queries {
+    uint32_t f[NT == 1 ? D / 32 : 1][4];
+    const uint4 *s;   // this lane's entry of (word 0, this warp's first n-tile)
+};
+
+// A unit's S^T = K Q^T
+template <int D, int NT, int RW>
+__device__ __forceinline__ void scores(const KFrag<D> (&f)[kUnitTiles], uint32_t ks_sel, const Queries<D, NT> &q,
+                                       float (&sc)[NT][kUnitTiles][4])
 {
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[j][k][e] = 0.f;
+        for (int k = 0; k < kUnitTiles; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[j][k][e] = 0.f;
 #pragma unroll
     for (int w = 0; w < KFrag<D>::KW; ++w) {
-        // the block's scale of this lane's two rows, in both halves
-        const uint32_t sb = __byte_perm(f.s[w / 2], 0u, ks_sel);
-        const uint32_t s0 = cvt_lo(sb), s1 = cvt_hi(sb);
-        const uint32_t x0 = f.x[0][w], x1 = f.x[1][w];
-        const uint32_t lo[4] = {hmul2(e2m1_pair<0>(x0), s0), hmul2(e2m1_pair<0>(x1), s1),
-                                hmul2(e2m1_pair<1>(x0), s0), hmul2(e2m1_pair<1>(x1), s1)};
-        const uint32_t hi[4] = {hmul2(e2m1_pair<2>(x0), s0), hmul2(e2m1_pair<2>(x1), s1),
-                                hmul2(e2m1_pair<3>(x0), s0), hmul2(e2m1_pair<3>(x1), s1)};
+        uint32_t lo[kUnitTiles][4], hi[kUnitTiles][4];
+#pragma unroll
+        for (int k = 0; k < kUnitTiles; ++k) {
+            // the block's scale of this lane's two rows, in both halves
+            const uint32_t sb = __byte_perm(f[k].s[w / 2], 0u, ks_sel);
+            const uint32_t s0 = cvt_lo(sb), s1 = cvt_hi(sb);
+            const uint32_t x0 = f[k].x[0][w], x1 = f[k].x[1][w];
+            lo[k][0] = hmul2(e2m1_pair<0>(x0), s0);
+            lo[k][1] = hmul2(e2m1_pair<0>(x1), s1);
+            lo[k][2] = hmul2(e2m1_pair<1>(x0), s0);
+            lo[k][3] = hmul2(e2m1_pair<1>(x1), s1);
+            hi[k][0] = hmul2(e2m1_pair<2>(x0), s0);
+            hi[k][1] = hmul2(e2m1_pair<2>(x1), s1);
+            hi[k][2] = hmul2(e2m1_pair<3>(x0), s0);
+            hi[k][3] = hmul2(e2m1_pair<3>(x1), s1);
+        }
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            mma_16816(sc[j][k], lo, qf[j][2 * w][0], qf[j][2 * w][1]);
-            mma_16816(sc[j][k], hi, qf[j][2 * w + 1][0], qf[j][2 * w + 1][1]);
+            uint32_t b[4];
+            if constexpr (NT == 1) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) b[e] = q.f[w][e];
+            } else {
+                const uint4 v = q.s[(w * RW * NT + j) * 32];
+                b[0] = v.x;
+                b[1] = v.y;
+                b[2] = v.z;
+                b[3] = v.w;
+            }
+#pragma unroll
+            for (int k = 0; k < kUnitTiles; ++k) {
+                mma_16816(sc[j][k], lo[k], b[0], b[1]);
+                mma_16816(sc[j][k], hi[k], b[2], b[3]);
+            }
         }
     }
 }
@@ -229,7 +265,7 @@ __device__ __forceinline__ void softmax_unit(const float (&sc)[NT][kUnitTiles][4
 // NT n-tiles of 8 query rows per warp; RW warps share the same tokens and split
 // the query rows, the kQWarps / RW groups of warps split the tokens.
 template <int D, int NT, int RW>
-__global__ void __launch_bounds__(kQThreads, NT == 1 ? 4 : 3) attn_e2m1_kernel(const AttnArgs a)
+__global__ void __launch_bounds__(kQThreads, ctas_per_sm<NT>()) attn_e2m1_kernel(const AttnArgs a)
 {
     constexpr int TW = kQWarps / RW;
     constexpr int kRowsPad = RW * NT * 8;
@@ -238,7 +274,7 @@ __global__ void __launch_bounds__(kQThreads, NT == 1 ? 4 : 3) attn_e2m1_kernel(c
     constexpr int CPL = D / 4;                       // K channels per lane
     using KF = KFrag<D>;
     using VF = VFrag<D>;
-    using R = Ring<D>;
+    using R = Ring<D, NT>;
     extern __shared__ __align__(16) uint8_t smem[];
 
     const int s = blockIdx.x, g = blockIdx.y;
@@ -324,11 +360,9 @@ __global__ void __launch_bounds__(kQThreads, NT == 1 ? 4 : 3) attn_e2m1_kernel(c
 
     float o[NT][D / 16][4];
     float ref[NT][2], l_run[NT][2];       // log2-domain reference of a row, sum of its 2^(s - ref)
-    uint32_t qf[NT][D / 16][2];
     int lim[NT][2];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-        const int row = (rw * NT + j) * 8 + gid;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             const int r = (rw * NT + j) * 8 + 2 * t + c;
@@ -337,22 +371,33 @@ __global__ void __launch_bounds__(kQThreads, NT == 1 ? 4 : 3) attn_e2m1_kernel(c
             l_run[j][c] = 0.f;
         }
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-            qf[j][ks][0] = qf[j][ks][1] = 0u;
+        for (int pv = 0; pv < D / 16; ++pv)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[j][ks][e] = 0.f;
-        }
-        if (row < a.rows) {
-            const int i = row / a.group, h = g * a.group + row % a.group;
-            const __half *qrow = static_cast<const __half *>(a.q) +
-                                 (((int64_t)b * a.q_len + i) * a.num_q_heads + h) * D + t * CPL;
+            for (int e = 0; e < 4; ++e) o[j][pv][e] = 0.f;
+    }
+    // query row `row`'s channels t CPL + 8 w .. + 7: the B fragments of the two k-steps of word w
+    auto q_words = [&](int row, int w) {
+        if (row >= a.rows) return make_uint4(0u, 0u, 0u, 0u);
+        const int i = row / a.group, h = g * a.group + row % a.group;
+        return *reinterpret_cast<const uint4 *>(static_cast<const __half *>(a.q) +
+                                                (((int64_t)b * a.q_len + i) * a.num_q_heads + h) * D + t * CPL + 8 * w);
+    };
+    Queries<D, NT> qs;
+    if constexpr (NT == 1) {
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-                const uint2 v = *reinterpret_cast<const uint2 *>(qrow + 4 * ks);
-                qf[j][ks][0] = v.x;
-                qf[j][ks][1] = v.y;
-            }
+        for (int w = 0; w < KF::KW; ++w) {
+            const uint4 v = q_words(gid, w);
+            qs.f[w][0] = v.x;
+            qs.f[w][1] = v.y;
+            qs.f[w][2] = v.z;
+            qs.f[w][3] = v.w;
         }
+    } else {
+        uint4 *qm = reinterpret_cast<uint4 *>(smem + kQWarps * R::kBytes);
+        for (int i = warp; i < KF::KW * RW * NT; i += kQWarps)
+            qm[i * 32 + lane] = q_words((i % (RW * NT)) * 8 + gid, i / (RW * NT));
+        __syncthreads();
+        qs.s = qm + rw * NT * 32 + lane;
     }
     const float qk = a.qk_scale_log2;
     float sc[NT][kUnitTiles][4];
@@ -366,14 +411,16 @@ __global__ void __launch_bounds__(kQThreads, NT == 1 ? 4 : 3) attn_e2m1_kernel(c
             const int ahead = raw_page(u0 + (R::kUnits + 1) * step);
             copy_wait<R::kUnits - 1>();
             const uint8_t *un = ring + slot * R::kUnit;
+            {
+                KF f[kUnitTiles];
 #pragma unroll
-            for (int k = 0; k < kUnitTiles; ++k) {
-                const uint8_t *tl = un + k * R::kTile;
-                KF f;
-                load_words(f.x[0], tl + lane * R::kK);
-                load_words(f.x[1], tl + 32 * R::kK + lane * R::kK);
-                load_words(f.s, tl + R::kOffKS + lane * R::kKS);
-                scores<D, NT>(f, ks_sel, qf, sc, k);
+                for (int k = 0; k < kUnitTiles; ++k) {
+                    const uint8_t *tl = un + k * R::kTile;
+                    load_words(f[k].x[0], tl + lane * R::kK);
+                    load_words(f[k].x[1], tl + 32 * R::kK + lane * R::kK);
+                    load_words(f[k].s, tl + R::kOffKS + lane * R::kKS);
+                }
+                scores<D, NT, RW>(f, ks_sel, qs, sc);
             }
             const unsigned paged = __ballot_sync(kFull, pg[0] >= 0);   // bits 0..7 (and their copies): pages
             uint32_t vmask[kUnitTiles];
@@ -452,29 +499,32 @@ __global__ void __launch_bounds__(kQThreads, NT == 1 ? 4 : 3) attn_e2m1_kernel(c
                 }
                 vf[k].s &= byte_mask((live >> (16 * k + 4 * t)) & 15u);
             }
+            KF kf[kUnitTiles];
+            int row_pos[kUnitTiles][2];
 #pragma unroll
             for (int k = 0; k < kUnitTiles; ++k) {
-                KF f;
+                KF &f = kf[k];
 #pragma unroll
                 for (int w = 0; w < KF::KB; ++w) f.s[w] = 0u;
-                int row_pos[2];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const int e = 16 * k + 4 * (gid >> 1) + (gid & 1) + 2 * r;
                     const int p = __shfl_sync(kFull, pos, e), at = p & 3;
                     const uint8_t *row = kpool + (int64_t)__shfl_sync(kFull, phys, e) * page_stride;
-                    row_pos[r] = p >= 0 ? p : kNoToken;
+                    row_pos[k][r] = p >= 0 ? p : kNoToken;
                     load_words(f.x[r], row + k_code + at * (D / 2));
 #pragma unroll
                     for (int w = 0; w < KF::KB; ++w) f.s[w] |= (uint32_t)row[k_scale + 4 * w + at] << (8 * ((gid & 1) + 2 * r));
                 }
-                scores<D, NT>(f, ks_sel, qf, sc, k);
+            }
+            scores<D, NT, RW>(kf, ks_sel, qs, sc);
+#pragma unroll
+            for (int k = 0; k < kUnitTiles; ++k)
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (row_pos[e >> 1] > lim[j][e & 1]) sc[j][k][e] = -INFINITY;
-            }
+                        if (row_pos[k][e >> 1] > lim[j][e & 1]) sc[j][k][e] = -INFINITY;
             softmax_unit<D, NT>(sc, qk, ref, l_run, o, pf);
 #pragma unroll
             for (int k = 0; k < kUnitTiles; ++k) weigh<D, NT>(vf[k], pf, o, k);
@@ -543,7 +593,7 @@ __global__ void __launch_bounds__(kQThreads, NT == 1 ? 4 : 3) attn_e2m1_kernel(c
 template <int D, int NT, int RW>
 static cudaError_t launch_e2m1(const AttnArgs &a, cudaStream_t stream)
 {
-    constexpr int merge = kQWarps * NT * 8 * (D + 4) * 4, ring = kQWarps * Ring<D>::kBytes;
+    constexpr int merge = kQWarps * NT * 8 * (D + 4) * 4, ring = kQWarps * Ring<D, NT>::kBytes + q_bytes<D, NT, RW>();
     constexpr int bytes = merge > ring ? merge : ring;
     static uint64_t configured = 0;   // one bit per device ordinal
     int dev = 0;
@@ -564,8 +614,9 @@ static cudaError_t launch_e2m1_rows(const AttnArgs &a, cudaStream_t stream)
     const int tiles = (a.rows + 7) / 8;
     if (tiles <= 1) return launch_e2m1<D, 1, 1>(a, stream);
     if (tiles <= 2) return launch_e2m1<D, 2, 1>(a, stream);
-    if (tiles <= 4) return launch_e2m1<D, 2, 2>(a, stream);
-    return launch_e2m1<D, 2, 4>(a, stream);
+    if (tiles <= 3) return launch_e2m1<D, 3, 1>(a, stream);
+    if (tiles <= 4) return launch_e2m1<D, 4, 1>(a, stream);
+    return launch_e2m1<D, 4, 2>(a, stream);
 }
 
 cudaError_t launch_attention_e2m1(int head_dim, const AttnArgs &a, cudaStream_t stream)
