@@ -5,7 +5,8 @@
 Each .cu file under csrc/ compiles in its own nvcc process (in parallel);
 the objects link into fp8_paged_kv_e4m3_gb300/_build/libkvq.so with the
 CUDA runtime linked statically.  No torch headers are involved: the library
-is a plain C ABI.
+is a plain C ABI.  kvq_pycall.c, the CPython module that marshals some calls,
+compiles to _build/kvq_pycall.so.
 """
 from __future__ import annotations
 
@@ -16,6 +17,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -23,6 +25,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libkvq.so")
+PYCALL = os.path.join(BUILD, "kvq_pycall.so")   # CPython module that marshals the calls (kvq_pycall.c)
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -41,15 +44,29 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) \
+    return _sources() + glob.glob(os.path.join(CSRC, "*.c")) + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) \
         + glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(PYCALL):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(PYCALL))
     return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def _build_pycall() -> None:
+    cc = shutil.which("cc") or shutil.which("gcc")
+    if not cc:
+        raise RuntimeError("no C compiler: the call module cannot be built")
+    tmp = PYCALL + f".{os.getpid()}.tmp"
+    cmd = [cc, "-O2", "-std=gnu11", "-shared", "-fPIC", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "kvq_pycall.c"), "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stderr)
+        raise RuntimeError("cc failed:\n" + " ".join(cmd))
+    os.replace(tmp, PYCALL)
 
 
 def build(force: bool = False, ptxas_verbose: bool = False) -> str:
@@ -78,6 +95,7 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
     if r.returncode != 0:
         sys.stderr.write(r.stderr)
         raise RuntimeError("link failed")
+    _build_pycall()
     os.replace(tmp, LIB)
     return LIB
 

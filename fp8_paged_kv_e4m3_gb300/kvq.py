@@ -9,6 +9,7 @@ missing or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import os
 import threading
@@ -34,6 +35,7 @@ ROPE_SCALING = {None: 0, "linear": 1, "yarn": 2}
 
 _lock = threading.Lock()
 _lib = None
+_pycall = None      # the call module, once the default library is loaded
 
 
 class KvqError(RuntimeError):
@@ -78,7 +80,7 @@ EXPORTS = ("kvq_version", "kvq_status_string", "kvq_validate_scales", "kvq_amax_
 
 def load(path: Optional[str] = None):
     """Load libkvq.so (built by fp8_paged_kv_e4m3_gb300.build); raise if absent."""
-    global _lib
+    global _lib, _pycall
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -139,8 +141,32 @@ def load(path: Optional[str] = None):
                      "paged_prefill_attn_e2m1"):
             getattr(lib, name).restype = ctypes.c_int
         if path is None:
+            _pycall = _load_pycall(lib, os.path.join(os.path.dirname(p), "kvq_pycall.so"))
             _lib = lib
         return lib
+
+
+def _load_pycall(lib, path: str):
+    """The CPython module that marshals the E2M1 and rotary calls (kvq_pycall.c).  Its functions return a
+    status, or None for arguments that are not those of a plain call: the ctypes path then names them."""
+    if not os.path.exists(path):
+        raise RuntimeError(f"call module not built: {path} is missing (run `python -m fp8_paged_kv_e4m3_gb300.build`)")
+    spec = importlib.util.spec_from_file_location("kvq_pycall", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    entry = ("paged_decode_attn_e2m1", "paged_decode_attn_e2m1_partial", "paged_prefill_attn_e2m1", "kv_append_e2m1",
+             "kv_gather_e2m1", "kv_append_rope_e4m3", "kv_append_rope_e2m1", "kv_append_rope_fp16")
+    mod.setup(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in entry),
+              (torch.float16, torch.float32, torch.int32, torch.uint8), _raw_stream, torch.cuda.current_device)
+    return mod
+
+
+def _raw_stream(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):   # the same value, without a Python stream object
+    _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _check(fn: str, status: int):
@@ -605,6 +631,14 @@ def _heads(t, name: str):
 
 def _append_rope(fn, q, k_new, v_new, positions, table, slot_mapping, k_cache, v_cache, scales, dtype, e2m1, q_out,
                  interleaved, err_flag):
+    if _pycall is not None:
+        if q_out is None and q is not None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        st = _pycall.rope(2 if e2m1 else 1 if dtype is torch.float16 else 0, q, k_new, v_new, positions, table, slot_mapping,
+                          q_out, k_cache, v_cache, *(scales or (1.0, 1.0)), ROPE_INTERLEAVED if interleaved else 0, err_flag)
+        if st is not None:
+            _check(fn, st)
+            return q_out
     ks, vs = _heads(k_new, "k_new"), _heads(v_new, "v_new")
     if k_new.shape != v_new.shape:
         raise ValueError("k_new and v_new shapes differ")
@@ -688,6 +722,10 @@ def alloc_e2m1_pool(num_pages: int, num_kv_heads: int, head_dim: int, device="cu
 def kv_append_e2m1(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale: float, v_scale: float,
                    err_flag: Optional[torch.Tensor] = None) -> None:
     """Quantise fp16 K/V of new tokens [T, Hkv, D] into E2M1 pools."""
+    if _pycall is not None:
+        st = _pycall.append(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scale, err_flag)
+        if st is not None:
+            return _check("kv_append_e2m1", st)
     _need(k_new, "k_new", torch.float16, 3)
     _need(v_new, "v_new", torch.float16, 3)
     if k_new.shape != v_new.shape:
@@ -710,6 +748,11 @@ def kv_append_e2m1(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale: float,
 def kv_gather_e2m1(k_cache, v_cache, slots, k_scale: float, v_scale: float, k_out=None, v_out=None,
                    err_flag: Optional[torch.Tensor] = None):
     """The cached rows at `slots` as fp16 [T, Hkv, D] (K, V); zeros for a slot of -1."""
+    if _pycall is not None and k_out is not None and v_out is not None:
+        st = _pycall.gather(k_cache, v_cache, slots, k_scale, v_scale, k_out, v_out, err_flag)
+        if st is not None:
+            _check("kv_gather_e2m1", st)
+            return k_out, v_out
     _need(k_cache, "k_cache", torch.uint8, 3)
     D = k_cache.shape[2] * 4 // 9
     Hkv = _pools(k_cache, v_cache, torch.uint8, D, True)
@@ -741,6 +784,14 @@ def paged_decode_attn_e2m1(q, k_cache, v_cache, block_tables, context_lens, k_sc
                            out=None, topk_idx=None, topk_lens=None, num_splits: int = 0, sm_scale: float = 0.0,
                            err_flag=None, split_pages: int = 0, strict_order: bool = False):
     """paged_decode_attn_e4m3 over E2M1 pools [P, Hkv, 9 * D / 4]; returns `out` (fp16, shape of q)."""
+    if _pycall is not None:
+        if out is None:
+            out = torch.empty_like(q)
+        st = _pycall.decode(q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale, workspace, out, topk_idx,
+                            topk_lens, num_splits, sm_scale, err_flag, split_pages, ATTN_STRICT_ORDER if strict_order else 0)
+        if st is not None:
+            _check("paged_decode_attn_e2m1", st)
+            return out
     p = _attn_check(q, k_cache, v_cache, block_tables, context_lens, workspace, out, topk_idx, topk_lens, torch.uint8,
                     num_splits, sm_scale, split_pages, strict_order=strict_order, e2m1=True)
     _e2m1_devices(q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, context_lens=context_lens,
@@ -773,6 +824,14 @@ def paged_decode_attn_e2m1_partial(q, k_cache, v_cache, block_tables, context_le
 def paged_prefill_attn_e2m1(q, k_cache, v_cache, block_tables, context_lens, q_start, k_scale: float, v_scale: float,
                             workspace, out=None, max_q_len: Optional[int] = None, sm_scale: float = 0.0, err_flag=None):
     """paged_prefill_attn_e4m3 over E2M1 pools [P, Hkv, 288]."""
+    if _pycall is not None and max_q_len is not None:
+        if out is None:
+            out = torch.empty_like(q)
+        st = _pycall.prefill(q, k_cache, v_cache, block_tables, context_lens, q_start, k_scale, v_scale, workspace, out,
+                             max_q_len, sm_scale, err_flag)
+        if st is not None:
+            _check("paged_prefill_attn_e2m1", st)
+            return out
     p = _prefill_check(q, k_cache, v_cache, block_tables, context_lens, q_start, workspace, out, torch.uint8, max_q_len,
                        sm_scale, e2m1=True)
     _e2m1_devices(q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, context_lens=context_lens,
