@@ -167,11 +167,14 @@ static int run_attention(const AttnCall &c, bool with_combine)
         (c.out && !aligned16(c.out)) || !aligned16(c.workspace) || (c.k_new && !aligned16(c.k_new)) ||
         (c.v_new && !aligned16(c.v_new)))
         return KVQ_ERR_ALIGNMENT;
-    const int32_t S = resolve_splits(&p);
+    int32_t S = resolve_splits(&p);
     const int64_t rows_total = int64_t(p.batch) * p.num_q_heads * p.q_len;
     if (rows_total * S > INT32_MAX) return KVQ_ERR_UNSUPPORTED;   // partials are indexed in 32 bits
+    if (!c.workspace || c.workspace_bytes < workspace_layout(rows_total, S, p.head_dim).total) return KVQ_ERR_WORKSPACE;
+    // the E2M1 kernel's own choice, at most the number the workspace was sized for
+    if (c.e2m1 && with_combine && p.num_splits == 0 && p.split_pages == 0)
+        S = e2m1_splits(p.batch, p.num_kv_heads, int(p.num_q_heads / p.num_kv_heads) * p.q_len, S);
     const WorkspaceLayout wl = workspace_layout(rows_total, S, p.head_dim);
-    if (!c.workspace || c.workspace_bytes < wl.total) return KVQ_ERR_WORKSPACE;
     if (p.batch == 0) return KVQ_OK;
 
     const int G = p.num_q_heads / p.num_kv_heads;
@@ -221,7 +224,7 @@ static int run_attention(const AttnCall &c, bool with_combine)
     cudaStream_t stream = static_cast<cudaStream_t>(c.stream);
     bool merged = false;
     if (c.e2m1) {
-        if (launch_attention_e2m1(p.head_dim, a, stream) != cudaSuccess) return KVQ_ERR_CUDA;
+        if (launch_attention_e2m1(p.head_dim, a, stream, &merged) != cudaSuccess) return KVQ_ERR_CUDA;
     } else if (launch_attention(c.e4m3, p.head_dim, a, stream, &merged) != cudaSuccess) return KVQ_ERR_CUDA;
     if (with_combine && !merged &&
         launch_combine(a.ws_o, a.ws_m, a.ws_l, c.out, p.batch, p.q_len, p.num_q_heads, p.head_dim, S,

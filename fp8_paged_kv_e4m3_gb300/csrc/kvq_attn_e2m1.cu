@@ -7,7 +7,7 @@
 // products run on fp16 tensor-core instructions (mma.sync m16n8k16, tokens on
 // M, query rows on N) with binary32 sums and the layer scales hoisted.
 //
-// One CTA of 4 warps per (split, kv head, sequence); a warp takes units of 32
+// One CTA of W warps per (split, kv head, sequence); a warp takes units of 32
 // tokens (two tiles of four pages) and keeps its own softmax.  A thread loads
 // from global memory exactly the bytes of its own matrix fragments, so nothing
 // goes through shared memory and no warp waits for another until the merge:
@@ -30,10 +30,12 @@ namespace kvq {
 
 namespace {
 
-constexpr int kQWarps = 4;
-constexpr int kQThreads = 32 * kQWarps;
-// CTAs per SM, by registers: O takes D / 4 a thread and n-tile
-template <int NT> __host__ __device__ constexpr int ctas_per_sm() { return NT == 1 ? 4 : NT == 2 ? 3 : 2; }
+// CTAs of W warps per SM, by registers: O takes D / 4 a thread and n-tile
+template <int NT, int W> __host__ __device__ constexpr int ctas_per_sm()
+{
+    const int n = (NT == 1 ? 16 : NT == 2 ? 12 : 8) / W;
+    return n > 0 ? n : 1;
+}
 constexpr int kUnitTiles = 2;                   // 16-token tiles a warp takes at once
 constexpr int kUnitPages = 4 * kUnitTiles;
 static_assert(kUnitPages == 8, "a unit's 32 tokens have a lane each");
@@ -263,10 +265,14 @@ __device__ __forceinline__ void softmax_unit(const float (&sc)[NT][kUnitTiles][4
 }
 
 // NT n-tiles of 8 query rows per warp; RW warps share the same tokens and split
-// the query rows, the kQWarps / RW groups of warps split the tokens.
-template <int D, int NT, int RW>
-__global__ void __launch_bounds__(kQThreads, ctas_per_sm<NT>()) attn_e2m1_kernel(const AttnArgs a)
+// the query rows, the W / RW groups of warps split the tokens.
+// MERGE: the splits of one (sequence, kv head) are one thread-block cluster; after
+// a cluster barrier its CTAs merge the partials (the combine's function, hence
+// its bits) and write the output themselves.
+template <int D, int NT, int RW, int W, bool MERGE>
+__global__ void __launch_bounds__(32 * W, ctas_per_sm<NT, W>()) attn_e2m1_kernel(const AttnArgs a)
 {
+    constexpr int kQWarps = W, kQThreads = 32 * W;
     constexpr int TW = kQWarps / RW;
     constexpr int kRowsPad = RW * NT * 8;
     constexpr int kRowF = D + 4;                     // m, l, two unused, o[D]
@@ -303,12 +309,13 @@ __global__ void __launch_bounds__(kQThreads, ctas_per_sm<NT>()) attn_e2m1_kernel
     // --- dense: a unit is 8 pages; lane l (mod 8) holds page l's number (-1: none) ---
     const int step = TW * kUnitPages;
     int u0 = item0 + tw * kUnitPages;
+    const unsigned num_pages = (unsigned)min(a.num_pages, (int64_t)0x80000000ll);
     auto raw_page = [&](int u) {
         const int it = u + (lane & (kUnitPages - 1));
         return it < item1 ? __ldg(sr.bt_row + it) : -1;
     };
     auto checked = [&](int phys, int u) {
-        if (phys >= 0 && (int64_t)phys < a.num_pages) return phys;
+        if ((unsigned)phys < num_pages) return phys;
         if (u + (lane & (kUnitPages - 1)) < item1 && rw == 0 && lane < kUnitPages) report(a.err_flag, KVQ_DEV_BAD_PAGE);
         return -1;
     };
@@ -322,22 +329,23 @@ __global__ void __launch_bounds__(kQThreads, ctas_per_sm<NT>()) attn_e2m1_kernel
 #pragma unroll
         for (int k = 0; k < kUnitTiles; ++k) {
             const uint32_t dst = ring_s + slot * R::kUnit + k * R::kTile;
-            const int64_t kp = (int64_t)__shfl_sync(kFull, page, 4 * k + (gid >> 1)) * page_stride;
-            const int64_t vp = (int64_t)__shfl_sync(kFull, page, 4 * k + t) * page_stride;
-            copy_async<R::kK>(dst + lane * R::kK, k_rows + kp);
-            copy_async<R::kK>(dst + 32 * R::kK + lane * R::kK, k_rows + kp + D);
-            copy_async<R::kKS>(dst + R::kOffKS + lane * R::kKS, k_scales + kp);
+            // (a 32 x 32 -> 64-bit multiply-add each)
+            const int kp = __shfl_sync(kFull, page, 4 * k + (gid >> 1)), vp = __shfl_sync(kFull, page, 4 * k + t);
+            const uint8_t *kr = k_rows + (int64_t)kp * page_stride, *ks = k_scales + (int64_t)kp * page_stride;
+            const uint8_t *vr = v_rows + (int64_t)vp * page_stride, *vs = v_scales + (int64_t)vp * page_stride;
+            copy_async<R::kK>(dst + lane * R::kK, kr);
+            copy_async<R::kK>(dst + 32 * R::kK + lane * R::kK, kr + D);
+            copy_async<R::kKS>(dst + R::kOffKS + lane * R::kKS, ks);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                copy_async<R::kV>(dst + R::kOffV + j * 32 * R::kV + lane * R::kV, v_rows + vp + j * (D / 2));
-            copy_async<R::kVS>(dst + R::kOffVS + lane * R::kVS, v_scales + vp);
+            for (int j = 0; j < 4; ++j) copy_async<R::kV>(dst + R::kOffV + j * 32 * R::kV + lane * R::kV, vr + j * (D / 2));
+            copy_async<R::kVS>(dst + R::kOffVS + lane * R::kVS, vs);
         }
     };
-    int pg[R::kUnits + 1];                 // pages of the units in flight and of the one after
+    int pg[R::kUnits];                     // pages of the units in flight, the next one first
     bool waited = !early;
     if (!sr.topk) {
 #pragma unroll
-        for (int d = 0; d <= R::kUnits; ++d) pg[d] = raw_page(u0 + d * step);
+        for (int d = 0; d < R::kUnits; ++d) pg[d] = raw_page(u0 + d * step);
 #pragma unroll
         for (int d = 0; d < R::kUnits; ++d) {
             const int u = u0 + d * step;
@@ -360,13 +368,16 @@ __global__ void __launch_bounds__(kQThreads, ctas_per_sm<NT>()) attn_e2m1_kernel
 
     float o[NT][D / 16][4];
     float ref[NT][2], l_run[NT][2];       // log2-domain reference of a row, sum of its 2^(s - ref)
-    int lim[NT][2];
+    // last position that column c of n-tile j sees (rows that do not exist see everything);
+    // needed on masked units only
+    auto lim = [&](int j, int c) {
+        const int r = (rw * NT + j) * 8 + 2 * t + c;
+        return r < a.rows ? L - a.q_len + r / a.group : 0x7FFFFFFE;
+    };
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            const int r = (rw * NT + j) * 8 + 2 * t + c;
-            lim[j][c] = (r < a.rows) ? L - a.q_len + r / a.group : 0x7FFFFFFE;
             ref[j][c] = -INFINITY;
             l_run[j][c] = 0.f;
         }
@@ -405,10 +416,10 @@ __global__ void __launch_bounds__(kQThreads, ctas_per_sm<NT>()) attn_e2m1_kernel
     constexpr int kNoToken = 0x7FFFFFFF;   // a position beyond every row's limit
 
     if (!sr.topk) {
-        const int first_masked = L - a.q_len + 1;        // positions from here on are masked for some row
-        int slot = 0;
-        for (; u0 < item1; u0 += step) {
-            const int ahead = raw_page(u0 + (R::kUnits + 1) * step);
+        const int clean_end = (L - a.q_len + 1) / 4;     // pages below hold only positions that every row sees
+        for (int slot = 0; u0 < item1; u0 += step) {
+            const int u = u0 + R::kUnits * step;         // the unit this slot holds next
+            const int next = raw_page(u);
             copy_wait<R::kUnits - 1>();
             const uint8_t *un = ring + slot * R::kUnit;
             {
@@ -422,11 +433,11 @@ __global__ void __launch_bounds__(kQThreads, ctas_per_sm<NT>()) attn_e2m1_kernel
                 }
                 scores<D, NT, RW>(f, ks_sel, qs, sc);
             }
-            const unsigned paged = __ballot_sync(kFull, pg[0] >= 0);   // bits 0..7 (and their copies): pages
             uint32_t vmask[kUnitTiles];
 #pragma unroll
             for (int k = 0; k < kUnitTiles; ++k) vmask[k] = 0xFFFFFFFFu;
-            if (paged != kFull || u0 + kUnitPages > first_masked / 4) {
+            const unsigned paged = __ballot_sync(kFull, pg[0] >= 0);   // bits 0..7 (and their copies): pages
+            if (paged != kFull || u0 + kUnitPages > clean_end) {
                 // Slots without a token may hold any bits: their scores are replaced (whatever they
                 // are), and their V scales zeroed, since a NaN scale times a probability of 0 is NaN.
                 const unsigned live = __ballot_sync(kFull, ((paged >> (lane >> 2)) & 1u) && u0 * 4 + lane < L);
@@ -440,7 +451,7 @@ __global__ void __launch_bounds__(kQThreads, ctas_per_sm<NT>()) attn_e2m1_kernel
                         for (int j = 0; j < NT; ++j)
 #pragma unroll
                             for (int c = 0; c < 2; ++c)
-                                if (pos > lim[j][c]) sc[j][k][2 * r + c] = -INFINITY;
+                                if (pos > lim(j, c)) sc[j][k][2 * r + c] = -INFINITY;
                     }
                     vmask[k] = byte_mask((live >> (16 * k + 4 * t)) & 15u);
                 }
@@ -455,15 +466,13 @@ __global__ void __launch_bounds__(kQThreads, ctas_per_sm<NT>()) attn_e2m1_kernel
                 f.s = *reinterpret_cast<const uint32_t *>(tl + R::kOffVS + lane * R::kVS) & vmask[k];
                 weigh<D, NT>(f, pf, o, k);
             }
-            // this slot has been read (by this lane alone): the unit after those in flight
-            const int u = u0 + R::kUnits * step;
-            pg[R::kUnits] = checked(pg[R::kUnits], u);
-            if (u < item1) fetch(pg[R::kUnits], slot);
+            // this slot has been read (by this lane alone)
+#pragma unroll
+            for (int d = 0; d + 1 < R::kUnits; ++d) pg[d] = pg[d + 1];
+            pg[R::kUnits - 1] = checked(next, u);
+            if (u < item1) fetch(pg[R::kUnits - 1], slot);
             copy_commit();
             slot = slot + 1 == R::kUnits ? 0 : slot + 1;
-#pragma unroll
-            for (int d = 0; d < R::kUnits; ++d) pg[d] = pg[d + 1];
-            pg[R::kUnits] = ahead;
         }
     } else {
         // --- top-k: a unit is 32 list entries; entry 16 k + 4 p + j is token j of page slot p of
@@ -524,7 +533,7 @@ __global__ void __launch_bounds__(kQThreads, ctas_per_sm<NT>()) attn_e2m1_kernel
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (row_pos[k][e >> 1] > lim[j][e & 1]) sc[j][k][e] = -INFINITY;
+                        if (row_pos[k][e >> 1] > lim(j, e & 1)) sc[j][k][e] = -INFINITY;
             softmax_unit<D, NT>(sc, qk, ref, l_run, o, pf);
 #pragma unroll
             for (int k = 0; k < kUnitTiles; ++k) weigh<D, NT>(vf[k], pf, o, k);
@@ -586,43 +595,115 @@ __global__ void __launch_bounds__(kQThreads, ctas_per_sm<NT>()) attn_e2m1_kernel
         const float inv = a.out_scale / lsum;
         *reinterpret_cast<float4 *>(a.ws_o + unit * D + d) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     }
+    if constexpr (MERGE) {
+        cluster_barrier();   // release, then acquire: the cluster's workspace stores are visible
+        for (int row = s + S * warp; row < a.rows; row += S * kQWarps) {
+            const int i = row / a.group, h = g * a.group + row % a.group;
+            const int64_t r = ((int64_t)b * a.num_q_heads + h) * a.q_len + i;
+            float acc[D / 32];
+            const float sum = merge_splits<D>(a.ws_o + r * S * D, a.ws_m + r * S, a.ws_l + r * S, S, lane, 0, 1, acc);
+            store_merged<D>(static_cast<__half *>(a.out), b, i, h, a.q_len, a.num_q_heads, lane, acc, sum);
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------
 
-template <int D, int NT, int RW>
+template <int D, int NT, int RW, int W, bool MERGE>
 static cudaError_t launch_e2m1(const AttnArgs &a, cudaStream_t stream)
 {
-    constexpr int merge = kQWarps * NT * 8 * (D + 4) * 4, ring = kQWarps * Ring<D, NT>::kBytes + q_bytes<D, NT, RW>();
+    constexpr int merge = W * NT * 8 * (D + 4) * 4, ring = W * Ring<D, NT>::kBytes + q_bytes<D, NT, RW>();
     constexpr int bytes = merge > ring ? merge : ring;
+    static_assert(bytes <= 232448, "shared memory exceeds one CTA's limit");
     static uint64_t configured = 0;   // one bit per device ordinal
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 64 && !(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & (1ull << dev))) {
-        e = cudaFuncSetAttribute(attn_e2m1_kernel<D, NT, RW>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        e = cudaFuncSetAttribute(attn_e2m1_kernel<D, NT, RW, W, MERGE>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
         __atomic_fetch_or(&configured, 1ull << dev, __ATOMIC_ACQ_REL);
     }
-    return launch_pdl(attn_e2m1_kernel<D, NT, RW>, dim3(a.num_splits, a.num_kv_heads, a.batch), dim3(kQThreads), bytes,
-                      stream, a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.num_splits, a.num_kv_heads, a.batch);
+    cfg.blockDim = dim3(32 * W);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)a.num_splits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = MERGE ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, attn_e2m1_kernel<D, NT, RW, W, MERGE>, a);
 }
 
-template <int D>
+// The CTAs of W = 4 warps that are resident at once.
+static int64_t e2m1_resident(int rows)
+{
+    const int tiles = (rows + 7) / 8;
+    return int64_t(device_sm_count()) *
+           (tiles <= 1 ? ctas_per_sm<1, 4>() : tiles <= 2 ? ctas_per_sm<2, 4>() : ctas_per_sm<4, 4>());
+}
+
+// A grid that leaves most of the card idle takes wider CTAs: the same splits, each
+// walked by two or four times as many warps.
+template <int D, int NT, int RW, bool MERGE>
+static cudaError_t launch_e2m1_width(const AttnArgs &a, cudaStream_t stream)
+{
+    const int64_t ctas = int64_t(a.batch) * a.num_kv_heads * a.num_splits, resident = e2m1_resident(a.rows);
+    // (a cluster's CTAs share a GPC: one of more than four CTAs that each fill an SM may not find room)
+    if constexpr (NT == 1)
+        if (MERGE ? a.num_splits <= 4 && ctas <= 128 : ctas * 4 <= resident)
+            return launch_e2m1<D, NT, RW, 16, MERGE>(a, stream);
+    if (ctas * 2 <= resident) return launch_e2m1<D, NT, RW, 8, MERGE>(a, stream);
+    return launch_e2m1<D, NT, RW, 4, MERGE>(a, stream);
+}
+
+template <int D, bool MERGE>
 static cudaError_t launch_e2m1_rows(const AttnArgs &a, cudaStream_t stream)
 {
     const int tiles = (a.rows + 7) / 8;
-    if (tiles <= 1) return launch_e2m1<D, 1, 1>(a, stream);
-    if (tiles <= 2) return launch_e2m1<D, 2, 1>(a, stream);
-    if (tiles <= 3) return launch_e2m1<D, 3, 1>(a, stream);
-    if (tiles <= 4) return launch_e2m1<D, 4, 1>(a, stream);
-    return launch_e2m1<D, 4, 2>(a, stream);
+    if (tiles <= 1) return launch_e2m1_width<D, 1, 1, MERGE>(a, stream);
+    if (tiles <= 2) return launch_e2m1_width<D, 2, 1, MERGE>(a, stream);
+    if (tiles <= 3) return launch_e2m1_width<D, 3, 1, MERGE>(a, stream);
+    if (tiles <= 4) return launch_e2m1_width<D, 4, 1, MERGE>(a, stream);
+    return launch_e2m1_width<D, 4, 2, MERGE>(a, stream);
 }
 
-cudaError_t launch_attention_e2m1(int head_dim, const AttnArgs &a, cudaStream_t stream)
+int32_t e2m1_splits(int32_t batch, int32_t num_kv_heads, int rows, int32_t most)
 {
+    const int64_t pairs = int64_t(batch) * num_kv_heads, resident = e2m1_resident(rows);
+    int32_t best = most;
+    double score = 0.0;
+    for (int32_t s = most / 4 > 8 ? most / 4 : 8; s <= most; ++s) {
+        const int64_t ctas = pairs * s, waves = (ctas + resident - 1) / resident;
+        const double full = double(ctas) / double(waves * resident), v = full / (1.0 + 0.01 * s);
+        if (v > score) {
+            score = v;
+            best = s;
+        }
+    }
+    return best;
+}
+
+cudaError_t launch_attention_e2m1(int head_dim, const AttnArgs &a, cudaStream_t stream, bool *merged)
+{
+    *merged = false;
     if (a.batch == 0) return cudaSuccess;
-    return head_dim == 128 ? launch_e2m1_rows<128>(a, stream) : launch_e2m1_rows<64>(a, stream);
+    // Up to 8 splits are merged by their cluster, while the grid is resident at once: a CTA then waits
+    // at its end for the other splits of its (sequence, kv head), which finish at about the same time,
+    // instead of a second kernel that waits for all (B 32 x 4096: 21.8 -> 20.4 us).  On a grid of several
+    // waves it would hold a slot that the next wave needs (B 32 x 8192, 32 rows: 91 -> 106 us).
+    const int64_t ctas = int64_t(a.batch) * a.num_kv_heads * a.num_splits;
+    if (a.out && a.num_splits <= 8 && ctas <= e2m1_resident(a.rows)) {
+        *merged = true;
+        return head_dim == 128 ? launch_e2m1_rows<128, true>(a, stream) : launch_e2m1_rows<64, true>(a, stream);
+    }
+    return head_dim == 128 ? launch_e2m1_rows<128, false>(a, stream) : launch_e2m1_rows<64, false>(a, stream);
 }
 
 }  // namespace kvq

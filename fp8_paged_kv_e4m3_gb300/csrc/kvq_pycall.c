@@ -66,23 +66,24 @@ static int tensor(PyObject *o, PyObject *dtype, int dims, int heads, int64_t *de
     }
     for (int i = 0; i < dims; ++i) v->dim[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(a, i));
     Py_DECREF(a);
-    if (heads) v->stride = v->dim[1] * v->dim[2];
-    a = PyObject_CallMethodNoArgs(o, s_contiguous);
-    if (!a) return 0;
-    Py_DECREF(a);
-    if (a != Py_True) {
-        if (!heads) return 0;
+    if (heads) {
         a = PyObject_CallMethodNoArgs(o, s_stride);
         if (!a) return 0;
         const int tuple = PyTuple_Check(a) && PyTuple_GET_SIZE(a) == 3;
         int64_t st[3] = {0, 0, 0};
         for (int i = 0; tuple && i < 3; ++i) st[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(a, i));
         Py_DECREF(a);
-        if (!tuple || st[2] != 1 || (v->dim[1] > 1 && st[1] != v->dim[2])) return 0;
+        if (!tuple || (v->dim[2] > 1 && st[2] != 1) || (v->dim[1] > 1 && st[1] != v->dim[2])) return 0;
+        v->stride = v->dim[1] * v->dim[2];
         if (v->dim[0] > 1) {
-            if (st[0] < v->dim[1] * v->dim[2]) return 0;
+            if (st[0] < v->stride) return 0;
             v->stride = st[0];
         }
+    } else {
+        a = PyObject_CallMethodNoArgs(o, s_contiguous);
+        if (!a) return 0;
+        Py_DECREF(a);
+        if (a != Py_True) return 0;
     }
     a = PyObject_CallMethodNoArgs(o, s_pointer);
     if (!a) return 0;

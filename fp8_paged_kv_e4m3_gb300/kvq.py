@@ -631,14 +631,6 @@ def _heads(t, name: str):
 
 def _append_rope(fn, q, k_new, v_new, positions, table, slot_mapping, k_cache, v_cache, scales, dtype, e2m1, q_out,
                  interleaved, err_flag):
-    if _pycall is not None:
-        if q_out is None and q is not None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        st = _pycall.rope(2 if e2m1 else 1 if dtype is torch.float16 else 0, q, k_new, v_new, positions, table, slot_mapping,
-                          q_out, k_cache, v_cache, *(scales or (1.0, 1.0)), ROPE_INTERLEAVED if interleaved else 0, err_flag)
-        if st is not None:
-            _check(fn, st)
-            return q_out
     ks, vs = _heads(k_new, "k_new"), _heads(v_new, "v_new")
     if k_new.shape != v_new.shape:
         raise ValueError("k_new and v_new shapes differ")
@@ -684,6 +676,15 @@ def kv_append_rope_e4m3(q, k_new, v_new, positions, table, slot_mapping, k_cache
     interleaved: pairs (2j, 2j + 1) instead of (j, j + rot_dim / 2).  q, k_new
     and v_new may be slices of one packed projection; q_out may be q itself
     when that is contiguous.  Returns q_out."""
+    if _pycall is not None:
+        if q_out is None and q is not None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        st = _pycall.rope(0, q, k_new, v_new, positions, table, slot_mapping, q_out, k_cache, v_cache, k_scale, v_scale,
+                          ROPE_INTERLEAVED if interleaved else 0, err_flag)
+        if st == KVQ_OK:
+            return q_out
+        if st is not None:
+            raise KvqError("kv_append_rope_e4m3", st)
     return _append_rope("kv_append_rope_e4m3", q, k_new, v_new, positions, table, slot_mapping, k_cache, v_cache,
                         (k_scale, v_scale), torch.uint8, False, q_out, interleaved, err_flag)
 
@@ -691,6 +692,15 @@ def kv_append_rope_e4m3(q, k_new, v_new, positions, table, slot_mapping, k_cache
 def kv_append_rope_fp16(q, k_new, v_new, positions, table, slot_mapping, k_cache, v_cache, q_out=None,
                         interleaved: bool = False, err_flag: Optional[torch.Tensor] = None):
     """fp16-KV twin of kv_append_rope_e4m3."""
+    if _pycall is not None:
+        if q_out is None and q is not None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        st = _pycall.rope(1, q, k_new, v_new, positions, table, slot_mapping, q_out, k_cache, v_cache, 1.0, 1.0,
+                          ROPE_INTERLEAVED if interleaved else 0, err_flag)
+        if st == KVQ_OK:
+            return q_out
+        if st is not None:
+            raise KvqError("kv_append_rope_fp16", st)
     return _append_rope("kv_append_rope_fp16", q, k_new, v_new, positions, table, slot_mapping, k_cache, v_cache, (),
                         torch.float16, False, q_out, interleaved, err_flag)
 
@@ -698,6 +708,15 @@ def kv_append_rope_fp16(q, k_new, v_new, positions, table, slot_mapping, k_cache
 def kv_append_rope_e2m1(q, k_new, v_new, positions, table, slot_mapping, k_cache, v_cache, k_scale: float, v_scale: float,
                         q_out=None, interleaved: bool = False, err_flag: Optional[torch.Tensor] = None):
     """kv_append_rope_e4m3 into E2M1 pools."""
+    if _pycall is not None:
+        if q_out is None and q is not None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        st = _pycall.rope(2, q, k_new, v_new, positions, table, slot_mapping, q_out, k_cache, v_cache, k_scale, v_scale,
+                          ROPE_INTERLEAVED if interleaved else 0, err_flag)
+        if st == KVQ_OK:
+            return q_out
+        if st is not None:
+            raise KvqError("kv_append_rope_e2m1", st)
     return _append_rope("kv_append_rope_e2m1", q, k_new, v_new, positions, table, slot_mapping, k_cache, v_cache,
                         (k_scale, v_scale), torch.uint8, True, q_out, interleaved, err_flag)
 
