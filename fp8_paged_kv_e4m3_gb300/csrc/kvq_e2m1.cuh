@@ -26,7 +26,7 @@ __device__ __forceinline__ uint32_t e2m1_pack2(float lo, float hi)
     uint32_t d;
     asm("{\n\t.reg .b8 b, z;\n\tmov.b16 {z, b}, 0;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\tmov.b32 %0, {b, z, z, z};\n\t}"
         : "=r"(d) : "f"(lo), "f"(hi));
-    return d & 0xFFu;
+    return d;   // the other bytes are 0
 }
 
 // eight fp32 -> eight E2M1 codes (element 0 in the lowest nibble).  The bytes

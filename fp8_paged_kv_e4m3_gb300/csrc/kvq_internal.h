@@ -26,7 +26,7 @@ struct RopeArgs {
     int32_t num_tokens, num_q_heads, num_kv_heads, head_dim, rot_dim, max_positions;
     float k_scale, v_scale, k_six, v_six;   // *_six: fl(6 * scale), E2M1
     bool interleaved;
-    int32_t lanes, heads_per_warp, chunks;  // set by the launcher
+    int32_t q_chunks, rounds;               // set by the launcher
 };
 
 // Arguments of one split-K attention launch (device pointers).

@@ -54,160 +54,192 @@ __device__ __forceinline__ uint2 quantize8(const float (&y)[8], float scale)
 }  // namespace
 
 // ---------------------------------------------------------------------------
-// Append with the rotation on the way.  A token's heads are its queries (Hq),
-// keys (Hkv) and values (Hkv); a lane owns 8 consecutive channels of a head, a
-// warp holds whole heads (D / 8 lanes each), so that a pair's other half comes
-// from a lane of the warp (half layout: half / 8 lanes away; interleaved: the
-// lane itself) and rotating the queries in place is safe: every load precedes
-// the shuffles, every store follows them.  A warp takes kIter groups of heads
-// of one token, loading all of them before the table entries, which it reads
-// once for all.  ROTATE = false is the plain append (keys and values only).
+// Append with the rotation on the way.  A lane owns 8 consecutive channels of a
+// head, a warp holds whole heads (D / 8 lanes each), so that a pair's other half
+// comes from a lane of the warp (half layout: half / 8 lanes away; interleaved:
+// the lane itself) and rotating the queries in place is safe: every load precedes
+// the shuffles, every store follows them.  A warp takes one token and, by
+// blockIdx.y, some of its query heads or of its key and value heads, kIter groups
+// of heads at a time: all of a group's loads first, the table entries (which every
+// head of the token shares) once.  D = 0: any head_dim.
 constexpr int kIter = 4;
 
-template <PoolKind POOL, bool ROTATE>
+// max |x| over eight values, as binary32 bits; NaN if any is (maximum of three, sm_100 and later)
+__device__ __forceinline__ uint32_t absmax8_bits(const float (&x)[8])
+{
+    float a, b, c;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(a) : "f"(x[0]), "f"(x[1]), "f"(x[2]));
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(b) : "f"(x[3]), "f"(x[4]), "f"(x[5]));
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(c) : "f"(x[6]), "f"(x[7]), "f"(a));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(b), "f"(c));
+    return __float_as_uint(a);
+}
+
+// c, s: this lane's table entries, s with the sign of its half: out = fl(x c) + fl(partner s).
+// (As packed two-lane multiplies and adds this is compiled to fused multiply-adds, which
+// round once: the scalar intrinsics keep the three roundings of the definition.)
+__device__ __forceinline__ void rotate8(float (&x)[8], uint4 other, bool interleaved, const float (&c)[8], const float (&s)[8])
+{
+    float p[8];
+    unpack8(other, p);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        x[j] = __fadd_rn(__fmul_rn(x[j], c[j]), __fmul_rn(interleaved ? p[j ^ 1] : p[j], s[j]));
+}
+
+template <PoolKind POOL, bool ROTATE, int D>
 __global__ void __launch_bounds__(kRopeThreads) append_rope_kernel(const RopeArgs a)
 {
     grid_dependency_wait();   // the projections and indices may come from the previous kernel
     launch_dependents();
+    const int head_dim = D ? D : a.head_dim;
+    const int lanes = head_dim / 8, hpw = 32 / lanes;   // lanes per head, heads per warp
     const int lane = threadIdx.x & 31;
-    const int64_t w = ((int64_t)blockIdx.x * kRopeThreads + threadIdx.x) >> 5;
-    const int64_t token = w / a.chunks;
+    const int64_t token = (int64_t)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
     if (token >= a.num_tokens) return;
-    const int chunk = (int)(w - token * a.chunks);
-    const int sub = lane / a.lanes;                    // which of the warp's heads this lane belongs to
-    const int vec = lane - sub * a.lanes;
-    const bool live = sub < a.heads_per_warp;          // lanes past the last whole head idle
+    const int sub = lane / lanes, vec = lane - sub * lanes;   // the warp's head this lane belongs to, its vector
     const int ch = vec * 8;
-    const int heads = a.num_q_heads + 2 * a.num_kv_heads;
-    const int32_t slot = __ldg(a.slots + token);
+    const bool live = sub < hpw;                        // lanes past the last whole head idle
+    const bool is_q = ROTATE && (int)blockIdx.y < a.q_chunks;
+    const int chunk = is_q ? blockIdx.y : blockIdx.y - (ROTATE ? a.q_chunks : 0);
+    const int heads = is_q ? a.num_q_heads : 2 * a.num_kv_heads;
+    const int h0 = chunk * (a.rounds * kIter) * hpw + sub;
     const int pos = ROTATE ? __ldg(a.positions + token) : 0;
-    if (ROTATE && (pos < 0 || pos >= a.max_positions)) {   // the same on every lane
-        if (chunk == 0 && lane == 0) report(a.err_flag, KVQ_DEV_BAD_POS);
-        return;
-    }
+    const int32_t slot = is_q ? 0 : __ldg(a.slots + token);
     const int64_t page = slot >> 2;
-    const bool keep = slot >= 0 && page < a.num_pages;
-    if (slot >= 0 && !keep && chunk == 0 && lane == 0) report(a.err_flag, KVQ_DEV_BAD_SLOT);
+    const bool keep = !is_q && slot >= 0 && page < a.num_pages;
 
-    uint4 raw[kIter];
-    int head[kIter];
-#pragma unroll
-    for (int i = 0; i < kIter; ++i) {
-        const int h = (chunk * kIter + i) * a.heads_per_warp + sub;
-        head[i] = live && h < heads ? h : -1;
-        raw[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (head[i] < 0) continue;
-        const int hk = h - a.num_q_heads, hv = hk - a.num_kv_heads;
-        const __half *src = hk < 0 ? a.q + token * a.q_stride + (int64_t)h * a.head_dim
-                                   : hv < 0 ? a.k + token * a.k_stride + (int64_t)hk * a.head_dim
-                                            : a.v + token * a.v_stride + (int64_t)hv * a.head_dim;
-        raw[i] = *reinterpret_cast<const uint4 *>(src + ch);
-    }
-    // this lane's table entries: out = fl(x c) + fl(partner s), s carrying the sign
-    float c[8], s[8];
     const int half = a.rot_dim / 2;
     const bool turns = ROTATE && ch < a.rot_dim;
-    if (turns) {
-        const float *row = a.table + (int64_t)pos * a.rot_dim;
-        if (a.interleaved) {
-            const float4 cc = __ldg(reinterpret_cast<const float4 *>(row + ch / 2));
-            const float4 ss = __ldg(reinterpret_cast<const float4 *>(row + half + ch / 2));
-            const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                c[j] = cv[j / 2];
-                s[j] = (j & 1) ? sv[j / 2] : -sv[j / 2];
-            }
-        } else {
-            const bool first = ch < half;
-            const int at = first ? ch : ch - half;
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const float4 cc = __ldg(reinterpret_cast<const float4 *>(row + at) + q);
-                const float4 ss = __ldg(reinterpret_cast<const float4 *>(row + half + at) + q);
-                const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    c[4 * q + j] = cv[j];
-                    s[4 * q + j] = first ? -sv[j] : sv[j];
-                }
-            }
-        }
-    }
     const int mate = a.interleaved || !turns ? lane : (ch < half ? lane + half / 8 : lane - half / 8);
+    float c[8], s[8];
+    bool first_round = true;
+#pragma unroll 1
+    for (int r = 0; r < a.rounds; ++r) {
+        uint4 raw[kIter];
 #pragma unroll
-    for (int i = 0; i < kIter; ++i) {
-        uint4 other = raw[i];
-        if (ROTATE && !a.interleaved) {
-            other.x = __shfl_sync(kAll, raw[i].x, mate);
-            other.y = __shfl_sync(kAll, raw[i].y, mate);
-            other.z = __shfl_sync(kAll, raw[i].z, mate);
-            other.w = __shfl_sync(kAll, raw[i].w, mate);
+        for (int i = 0; i < kIter; ++i) {
+            const int h = h0 + (r * kIter + i) * hpw;
+            raw[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (!live || h >= heads) continue;
+            const int hv = h - a.num_kv_heads;
+            const __half *src = is_q ? a.q + token * a.q_stride + h * head_dim
+                                     : hv < 0 ? a.k + token * a.k_stride + h * head_dim : a.v + token * a.v_stride + hv * head_dim;
+            raw[i] = *reinterpret_cast<const uint4 *>(src + ch);
         }
-        const int h = head[i], hk = h - a.num_q_heads, hv = hk - a.num_kv_heads;
-        float x[8];
-        unpack8(raw[i], x);
-        if (turns && hv < 0) {
-            float p[8];
-            unpack8(other, p);
-            if (a.interleaved) {
+        if (first_round) {
+            first_round = false;
+            if (ROTATE && (unsigned)pos >= (unsigned)a.max_positions) {   // the same on every lane
+                if (blockIdx.y == 0 && lane == 0) report(a.err_flag, KVQ_DEV_BAD_POS);
+                return;
+            }
+            if (!is_q && slot >= 0 && !keep && chunk == 0 && lane == 0) report(a.err_flag, KVQ_DEV_BAD_SLOT);
+            if (turns) {
+                const float *row = a.table + (int64_t)pos * a.rot_dim;
+                if (a.interleaved) {
+                    const float4 cc = __ldg(reinterpret_cast<const float4 *>(row + ch / 2));
+                    const float4 ss = __ldg(reinterpret_cast<const float4 *>(row + half + ch / 2));
+                    const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
 #pragma unroll
-                for (int j = 0; j < 8; j += 2) {
-                    const float t = p[j];
-                    p[j] = p[j + 1];
-                    p[j + 1] = t;
+                    for (int j = 0; j < 8; ++j) {
+                        c[j] = cv[j / 2];
+                        s[j] = (j & 1) ? sv[j / 2] : -sv[j / 2];
+                    }
+                } else {
+                    const bool lower = ch < half;
+                    const int at = lower ? ch : ch - half;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const float4 cc = __ldg(reinterpret_cast<const float4 *>(row + at) + q);
+                        const float4 ss = __ldg(reinterpret_cast<const float4 *>(row + half + at) + q);
+                        const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            c[4 * q + j] = cv[j];
+                            s[4 * q + j] = lower ? -sv[j] : sv[j];
+                        }
+                    }
                 }
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = __fadd_rn(__fmul_rn(x[j], c[j]), __fmul_rn(p[j], s[j]));
         }
-        if (POOL == PoolKind::e2m1) {
-            // the block of 16: this lane's eight channels and its neighbour's
-            uint32_t m = 0u;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(x[j]) & 0x7FFFFFFFu);
-            m = max(m, __shfl_xor_sync(kAll, m, 1));
-            if (hk >= 0 && keep) {
-                const float scale = hv < 0 ? a.k_scale : a.v_scale;
-                const E2m1Block blk = e2m1_block(m, hv < 0 ? a.k_six : a.v_six, scale);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(x[j], blk.factor);
-                uint8_t *dst = static_cast<uint8_t *>(hv < 0 ? a.k_cache : a.v_cache) +
-                               (page * a.num_kv_heads + (hv < 0 ? hk : hv)) * e2m1_page_bytes(a.head_dim);
-                *reinterpret_cast<uint32_t *>(dst + (slot & 3) * (a.head_dim / 2) + ch / 2) = e2m1_pack8(x);
-                if ((vec & 1) == 0) dst[e2m1_scale_off(a.head_dim) + (ch / 16) * 4 + (slot & 3)] = (uint8_t)blk.scale;
+        for (int i = 0; i < kIter; ++i) {
+            const int h = h0 + (r * kIter + i) * hpw, hv = h - a.num_kv_heads;
+            const bool mine = live && h < heads;
+            uint4 other = raw[i];
+            if (ROTATE && !a.interleaved) {
+                other.x = __shfl_sync(kAll, raw[i].x, mate);
+                other.y = __shfl_sync(kAll, raw[i].y, mate);
+                other.z = __shfl_sync(kAll, raw[i].z, mate);
+                other.w = __shfl_sync(kAll, raw[i].w, mate);
             }
-        }
-        if (h < 0) continue;
-        if (hk < 0) {
-            *reinterpret_cast<uint4 *>(a.q_out + (token * a.num_q_heads + h) * a.head_dim + ch) = pack8(x);
-        } else if (POOL != PoolKind::e2m1 && keep) {
-            const int64_t at = ((page * a.num_kv_heads + (hv < 0 ? hk : hv)) * 4 + (slot & 3)) * a.head_dim + ch;
-            void *pool = hv < 0 ? a.k_cache : a.v_cache;
-            if (POOL == PoolKind::e4m3)
-                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(pool) + at) = quantize8(x, hv < 0 ? a.k_scale : a.v_scale);
-            else
-                *reinterpret_cast<uint4 *>(static_cast<__half *>(pool) + at) = pack8(x);
+            if (is_q) {
+                if (!mine) continue;
+                uint4 out = raw[i];
+                if (turns) {
+                    float x[8];
+                    unpack8(raw[i], x);
+                    rotate8(x, other, a.interleaved, c, s);
+                    out = pack8(x);
+                }
+                *reinterpret_cast<uint4 *>(a.q_out + (token * a.num_q_heads + h) * head_dim + ch) = out;
+                continue;
+            }
+            const bool is_v = hv >= 0;
+            float x[8];
+            if (POOL != PoolKind::fp16 || (turns && !is_v)) unpack8(raw[i], x);
+            if (turns && !is_v) rotate8(x, other, a.interleaved, c, s);
+            const int64_t unit = page * a.num_kv_heads + (is_v ? hv : h);   // (page, kv head)
+            void *pool = is_v ? a.v_cache : a.k_cache;
+            if constexpr (POOL == PoolKind::e2m1) {
+                // the block of 16: this lane's eight channels and its neighbour's
+                uint32_t m = absmax8_bits(x);
+                m = max(m, __shfl_xor_sync(kAll, m, 1));
+                if (mine && keep) {
+                    const E2m1Block blk = e2m1_block(m, is_v ? a.v_six : a.k_six, is_v ? a.v_scale : a.k_scale);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(x[j], blk.factor);
+                    uint8_t *dst = static_cast<uint8_t *>(pool) + unit * e2m1_page_bytes(head_dim);
+                    *reinterpret_cast<uint32_t *>(dst + (slot & 3) * (head_dim / 2) + ch / 2) = e2m1_pack8(x);
+                    if ((vec & 1) == 0) dst[e2m1_scale_off(head_dim) + (ch / 16) * 4 + (slot & 3)] = (uint8_t)blk.scale;
+                }
+            } else if (mine && keep) {
+                const int64_t at = (unit * 4 + (slot & 3)) * head_dim + ch;
+                if constexpr (POOL == PoolKind::e4m3)
+                    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(pool) + at) = quantize8(x, is_v ? a.v_scale : a.k_scale);
+                else
+                    *reinterpret_cast<uint4 *>(static_cast<__half *>(pool) + at) = turns && !is_v ? pack8(x) : raw[i];
+            }
         }
     }
 }
 
+template <PoolKind POOL, bool ROTATE>
+static cudaError_t launch_append_rope_dim(dim3 grid, const RopeArgs &a, cudaStream_t stream)
+{
+    const dim3 block(kRopeThreads);
+    if (a.head_dim == 128) return launch_pdl(append_rope_kernel<POOL, ROTATE, 128>, grid, block, 0, stream, a);
+    if (a.head_dim == 64) return launch_pdl(append_rope_kernel<POOL, ROTATE, 64>, grid, block, 0, stream, a);
+    if constexpr (POOL != PoolKind::e2m1)
+        return launch_pdl(append_rope_kernel<POOL, ROTATE, 0>, grid, block, 0, stream, a);
+    return cudaErrorInvalidValue;
+}
+
 cudaError_t launch_append_rope(PoolKind pool, bool rotate, RopeArgs a, cudaStream_t stream)
 {
-    a.lanes = a.head_dim / 8;
-    a.heads_per_warp = 32 / a.lanes;
-    const int heads = a.num_q_heads + 2 * a.num_kv_heads;
-    const int groups = (heads + a.heads_per_warp - 1) / a.heads_per_warp;
-    a.chunks = (groups + kIter - 1) / kIter;
-    const int64_t warps = (int64_t)a.num_tokens * a.chunks;
-    const int64_t blocks = (warps * 32 + kRopeThreads - 1) / kRopeThreads;
-    if (blocks == 0) return cudaSuccess;
-    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    const dim3 grid((unsigned)blocks), block(kRopeThreads);
-    if (!rotate) return launch_pdl(append_rope_kernel<PoolKind::e2m1, false>, grid, block, 0, stream, a);
-    if (pool == PoolKind::e2m1) return launch_pdl(append_rope_kernel<PoolKind::e2m1, true>, grid, block, 0, stream, a);
-    if (pool == PoolKind::e4m3) return launch_pdl(append_rope_kernel<PoolKind::e4m3, true>, grid, block, 0, stream, a);
-    return launch_pdl(append_rope_kernel<PoolKind::fp16, true>, grid, block, 0, stream, a);
+    if (a.num_tokens == 0) return cudaSuccess;
+    const int hpw = 32 / (a.head_dim / 8);
+    // one round of kIter groups a warp while the warps are few, up to two where they fill the card
+    a.rounds = (int64_t)a.num_tokens * (a.num_q_heads + 2 * a.num_kv_heads) > (int64_t)device_sm_count() * 64 * 2 * kIter * hpw ? 2 : 1;
+    const int per = a.rounds * kIter * hpw;   // heads of a warp
+    a.q_chunks = (a.num_q_heads + per - 1) / per;
+    const int kv_chunks = (2 * a.num_kv_heads + per - 1) / per;
+    const dim3 grid((unsigned)((a.num_tokens + kRopeThreads / 32 - 1) / (kRopeThreads / 32)), (unsigned)(a.q_chunks + kv_chunks));
+    if (grid.y > 65535u) return cudaErrorInvalidConfiguration;
+    if (!rotate) return launch_append_rope_dim<PoolKind::e2m1, false>(grid, a, stream);
+    if (pool == PoolKind::e2m1) return launch_append_rope_dim<PoolKind::e2m1, true>(grid, a, stream);
+    if (pool == PoolKind::e4m3) return launch_append_rope_dim<PoolKind::e4m3, true>(grid, a, stream);
+    return launch_append_rope_dim<PoolKind::fp16, true>(grid, a, stream);
 }
 
 // ---------------------------------------------------------------------------
