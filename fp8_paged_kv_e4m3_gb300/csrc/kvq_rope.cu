@@ -87,8 +87,45 @@ __device__ __forceinline__ void rotate8(float (&x)[8], uint4 other, bool interle
         x[j] = __fadd_rn(__fmul_rn(x[j], c[j]), __fmul_rn(interleaved ? p[j ^ 1] : p[j], s[j]));
 }
 
+// This lane's table entries for position `pos`: c, and s with the sign of the lane's half.
+__device__ __forceinline__ void load_turn(const RopeArgs &a, int pos, int ch, float (&c)[8], float (&s)[8])
+{
+    const int half = a.rot_dim / 2;
+    const float *row = a.table + (int64_t)pos * a.rot_dim;
+    if (a.interleaved) {
+        const float4 cc = __ldg(reinterpret_cast<const float4 *>(row + ch / 2));
+        const float4 ss = __ldg(reinterpret_cast<const float4 *>(row + half + ch / 2));
+        const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            c[j] = cv[j / 2];
+            s[j] = (j & 1) ? sv[j / 2] : -sv[j / 2];
+        }
+    } else {
+        const bool lower = ch < half;
+        const int at = lower ? ch : ch - half;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const float4 cc = __ldg(reinterpret_cast<const float4 *>(row + at) + q);
+            const float4 ss = __ldg(reinterpret_cast<const float4 *>(row + half + at) + q);
+            const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                c[4 * q + j] = cv[j];
+                s[4 * q + j] = lower ? -sv[j] : sv[j];
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ uint4 shuffle4(uint4 v, int lane)
+{
+    return make_uint4(__shfl_sync(kAll, v.x, lane), __shfl_sync(kAll, v.y, lane), __shfl_sync(kAll, v.z, lane),
+                      __shfl_sync(kAll, v.w, lane));
+}
+
 template <PoolKind POOL, bool ROTATE, int D>
-__global__ void __launch_bounds__(kRopeThreads) append_rope_kernel(const RopeArgs a)
+__global__ void __launch_bounds__(kRopeThreads, 4) append_rope_kernel(const RopeArgs a)
 {
     grid_dependency_wait();   // the projections and indices may come from the previous kernel
     launch_dependents();
@@ -100,115 +137,115 @@ __global__ void __launch_bounds__(kRopeThreads) append_rope_kernel(const RopeArg
     const int sub = lane / lanes, vec = lane - sub * lanes;   // the warp's head this lane belongs to, its vector
     const int ch = vec * 8;
     const bool live = sub < hpw;                        // lanes past the last whole head idle
-    const bool is_q = ROTATE && (int)blockIdx.y < a.q_chunks;
-    const int chunk = is_q ? blockIdx.y : blockIdx.y - (ROTATE ? a.q_chunks : 0);
-    const int heads = is_q ? a.num_q_heads : 2 * a.num_kv_heads;
-    const int h0 = chunk * (a.rounds * kIter) * hpw + sub;
+    const int within = sub * head_dim + ch;             // this lane's place in a group of hpw heads
+    const int group_dim = hpw * head_dim;
     const int pos = ROTATE ? __ldg(a.positions + token) : 0;
-    const int32_t slot = is_q ? 0 : __ldg(a.slots + token);
-    const int64_t page = slot >> 2;
-    const bool keep = !is_q && slot >= 0 && page < a.num_pages;
-
-    const int half = a.rot_dim / 2;
+    const bool pos_ok = !ROTATE || (unsigned)pos < (unsigned)a.max_positions;
     const bool turns = ROTATE && ch < a.rot_dim;
+    const int half = a.rot_dim / 2;
     const int mate = a.interleaved || !turns ? lane : (ch < half ? lane + half / 8 : lane - half / 8);
     float c[8], s[8];
-    bool first_round = true;
+
+    if (ROTATE && (int)blockIdx.y < a.q_chunks) {
+        // ---- query heads: rotate into q_out ----
+        const int g0 = blockIdx.y * a.rounds * kIter;   // first group of heads
+        const __half *src = a.q + token * a.q_stride + (int64_t)g0 * group_dim + within;
+        __half *dst = a.q_out + token * a.num_q_heads * head_dim + (int64_t)g0 * group_dim + within;
+        const int left = live ? a.num_q_heads - g0 * hpw - sub : 0;   // head i * hpw exists while i * hpw < left
 #pragma unroll 1
-    for (int r = 0; r < a.rounds; ++r) {
-        uint4 raw[kIter];
+        for (int r = 0; r < a.rounds; ++r) {
+            uint4 raw[kIter];
 #pragma unroll
-        for (int i = 0; i < kIter; ++i) {
-            const int h = h0 + (r * kIter + i) * hpw;
-            raw[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (!live || h >= heads) continue;
-            const int hv = h - a.num_kv_heads;
-            const __half *src = is_q ? a.q + token * a.q_stride + h * head_dim
-                                     : hv < 0 ? a.k + token * a.k_stride + h * head_dim : a.v + token * a.v_stride + hv * head_dim;
-            raw[i] = *reinterpret_cast<const uint4 *>(src + ch);
-        }
-        if (first_round) {
-            first_round = false;
-            if (ROTATE && (unsigned)pos >= (unsigned)a.max_positions) {   // the same on every lane
-                if (blockIdx.y == 0 && lane == 0) report(a.err_flag, KVQ_DEV_BAD_POS);
-                return;
-            }
-            if (!is_q && slot >= 0 && !keep && chunk == 0 && lane == 0) report(a.err_flag, KVQ_DEV_BAD_SLOT);
-            if (turns) {
-                const float *row = a.table + (int64_t)pos * a.rot_dim;
-                if (a.interleaved) {
-                    const float4 cc = __ldg(reinterpret_cast<const float4 *>(row + ch / 2));
-                    const float4 ss = __ldg(reinterpret_cast<const float4 *>(row + half + ch / 2));
-                    const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        c[j] = cv[j / 2];
-                        s[j] = (j & 1) ? sv[j / 2] : -sv[j / 2];
-                    }
-                } else {
-                    const bool lower = ch < half;
-                    const int at = lower ? ch : ch - half;
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const float4 cc = __ldg(reinterpret_cast<const float4 *>(row + at) + q);
-                        const float4 ss = __ldg(reinterpret_cast<const float4 *>(row + half + at) + q);
-                        const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            c[4 * q + j] = cv[j];
-                            s[4 * q + j] = lower ? -sv[j] : sv[j];
-                        }
-                    }
+            for (int i = 0; i < kIter; ++i)
+                if ((r * kIter + i) * hpw < left) raw[i] = *reinterpret_cast<const uint4 *>(src + i * group_dim);
+            if (r == 0) {
+                if (!pos_ok) {                          // the same on every lane
+                    if (blockIdx.y == 0 && lane == 0) report(a.err_flag, KVQ_DEV_BAD_POS);
+                    return;
                 }
+                if (turns) load_turn(a, pos, ch, c, s);
             }
-        }
 #pragma unroll
-        for (int i = 0; i < kIter; ++i) {
-            const int h = h0 + (r * kIter + i) * hpw, hv = h - a.num_kv_heads;
-            const bool mine = live && h < heads;
-            uint4 other = raw[i];
-            if (ROTATE && !a.interleaved) {
-                other.x = __shfl_sync(kAll, raw[i].x, mate);
-                other.y = __shfl_sync(kAll, raw[i].y, mate);
-                other.z = __shfl_sync(kAll, raw[i].z, mate);
-                other.w = __shfl_sync(kAll, raw[i].w, mate);
-            }
-            if (is_q) {
-                if (!mine) continue;
-                uint4 out = raw[i];
+            for (int i = 0; i < kIter; ++i) {
+                uint4 other = raw[i];
+                if (!a.interleaved) other = shuffle4(raw[i], mate);
                 if (turns) {
                     float x[8];
                     unpack8(raw[i], x);
                     rotate8(x, other, a.interleaved, c, s);
-                    out = pack8(x);
+                    raw[i] = pack8(x);
                 }
-                *reinterpret_cast<uint4 *>(a.q_out + (token * a.num_q_heads + h) * head_dim + ch) = out;
-                continue;
+                if ((r * kIter + i) * hpw < left) *reinterpret_cast<uint4 *>(dst + i * group_dim) = raw[i];
             }
-            const bool is_v = hv >= 0;
+            src += kIter * group_dim;
+            dst += kIter * group_dim;
+        }
+        return;
+    }
+
+    // ---- key heads (rotated), then value heads, into the pools ----
+    const int32_t slot = __ldg(a.slots + token);
+    const int64_t page = slot >> 2;
+    const bool keep = slot >= 0 && page < a.num_pages;
+    const int chunk = blockIdx.y - (ROTATE ? a.q_chunks : 0);
+    if (lane == 0 && chunk == 0) {
+        if (!pos_ok && a.q_chunks == 0) report(a.err_flag, KVQ_DEV_BAD_POS);
+        if (pos_ok && slot >= 0 && !keep) report(a.err_flag, KVQ_DEV_BAD_SLOT);
+    }
+    if (!keep || !pos_ok) return;                       // the same on every lane
+    const int groups = (a.num_kv_heads + hpw - 1) / hpw;   // groups of key heads, and of value heads
+    const __half *ksrc = a.k + token * a.k_stride + within, *vsrc = a.v + token * a.v_stride + within;
+    const int64_t unit0 = page * a.num_kv_heads;        // (page, kv head 0)
+#pragma unroll 1
+    for (int r = 0; r < a.rounds; ++r) {
+        const int g0 = (chunk * a.rounds + r) * kIter;
+        uint4 raw[kIter];
+#pragma unroll
+        for (int i = 0; i < kIter; ++i) {
+            const int gi = g0 + i;
+            const bool is_v = gi >= groups;
+            const int g = is_v ? gi - groups : gi;
+            raw[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (live && g < groups && g * hpw + sub < a.num_kv_heads)
+                raw[i] = *reinterpret_cast<const uint4 *>((is_v ? vsrc : ksrc) + g * group_dim);
+        }
+        if (turns && g0 < groups) load_turn(a, pos, ch, c, s);
+#pragma unroll
+        for (int i = 0; i < kIter; ++i) {
+            const int gi = g0 + i;
+            if (gi >= 2 * groups) break;                // the same on every lane
+            const bool is_v = gi >= groups;
+            const int h = (is_v ? gi - groups : gi) * hpw + sub;
+            const bool mine = live && h < a.num_kv_heads;
             float x[8];
-            if (POOL != PoolKind::fp16 || (turns && !is_v)) unpack8(raw[i], x);
-            if (turns && !is_v) rotate8(x, other, a.interleaved, c, s);
-            const int64_t unit = page * a.num_kv_heads + (is_v ? hv : h);   // (page, kv head)
-            void *pool = is_v ? a.v_cache : a.k_cache;
+            unpack8(raw[i], x);
+            if (ROTATE && !is_v) {
+                uint4 other = raw[i];
+                if (!a.interleaved) other = shuffle4(raw[i], mate);
+                if (turns) {
+                    rotate8(x, other, a.interleaved, c, s);
+                    if (POOL == PoolKind::fp16) raw[i] = pack8(x);
+                }
+            }
+            uint8_t *pool = static_cast<uint8_t *>(is_v ? a.v_cache : a.k_cache);
+            const float scale = is_v ? a.v_scale : a.k_scale;
             if constexpr (POOL == PoolKind::e2m1) {
                 // the block of 16: this lane's eight channels and its neighbour's
                 uint32_t m = absmax8_bits(x);
                 m = max(m, __shfl_xor_sync(kAll, m, 1));
-                if (mine && keep) {
-                    const E2m1Block blk = e2m1_block(m, is_v ? a.v_six : a.k_six, is_v ? a.v_scale : a.k_scale);
+                if (!mine) continue;
+                const E2m1Block blk = e2m1_block(m, is_v ? a.v_six : a.k_six, scale);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(x[j], blk.factor);
-                    uint8_t *dst = static_cast<uint8_t *>(pool) + unit * e2m1_page_bytes(head_dim);
-                    *reinterpret_cast<uint32_t *>(dst + (slot & 3) * (head_dim / 2) + ch / 2) = e2m1_pack8(x);
-                    if ((vec & 1) == 0) dst[e2m1_scale_off(head_dim) + (ch / 16) * 4 + (slot & 3)] = (uint8_t)blk.scale;
-                }
-            } else if (mine && keep) {
-                const int64_t at = (unit * 4 + (slot & 3)) * head_dim + ch;
+                for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(x[j], blk.factor);
+                uint8_t *dst = pool + (unit0 + h) * e2m1_page_bytes(head_dim);
+                *reinterpret_cast<uint32_t *>(dst + (slot & 3) * (head_dim / 2) + ch / 2) = e2m1_pack8(x);
+                if ((vec & 1) == 0) dst[e2m1_scale_off(head_dim) + (ch / 16) * 4 + (slot & 3)] = (uint8_t)blk.scale;
+            } else if (mine) {
+                const int64_t at = ((unit0 + h) * 4 + (slot & 3)) * head_dim + ch;
                 if constexpr (POOL == PoolKind::e4m3)
-                    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(pool) + at) = quantize8(x, is_v ? a.v_scale : a.k_scale);
+                    *reinterpret_cast<uint2 *>(pool + at) = quantize8(x, scale);
                 else
-                    *reinterpret_cast<uint4 *>(static_cast<__half *>(pool) + at) = turns && !is_v ? pack8(x) : raw[i];
+                    *reinterpret_cast<uint4 *>(pool + 2 * at) = raw[i];
             }
         }
     }
@@ -233,7 +270,7 @@ cudaError_t launch_append_rope(PoolKind pool, bool rotate, RopeArgs a, cudaStrea
     a.rounds = (int64_t)a.num_tokens * (a.num_q_heads + 2 * a.num_kv_heads) > (int64_t)device_sm_count() * 64 * 2 * kIter * hpw ? 2 : 1;
     const int per = a.rounds * kIter * hpw;   // heads of a warp
     a.q_chunks = (a.num_q_heads + per - 1) / per;
-    const int kv_chunks = (2 * a.num_kv_heads + per - 1) / per;
+    const int kv_chunks = (2 * ((a.num_kv_heads + hpw - 1) / hpw) + a.rounds * kIter - 1) / (a.rounds * kIter);
     const dim3 grid((unsigned)((a.num_tokens + kRopeThreads / 32 - 1) / (kRopeThreads / 32)), (unsigned)(a.q_chunks + kv_chunks));
     if (grid.y > 65535u) return cudaErrorInvalidConfiguration;
     if (!rotate) return launch_append_rope_dim<PoolKind::e2m1, false>(grid, a, stream);
