@@ -282,57 +282,83 @@ cudaError_t launch_append_rope(PoolKind pool, bool rotate, RopeArgs a, cudaStrea
 // ---------------------------------------------------------------------------
 // Read-back: the rows of the listed slots as fp16, fl16(fl32(E2M1 * b) * S);
 // E2M1 * b has at most 6 significant bits, so the product with S is the only
-// binary32 rounding.  One thread per 8 channels of K or V (blockIdx.y).
-__global__ void __launch_bounds__(256) gather_e2m1_kernel(const uint8_t *__restrict__ k_cache,
-                                                          const uint8_t *__restrict__ v_cache, int64_t num_pages,
-                                                          const int32_t *__restrict__ slots, int64_t num_vecs,
-                                                          int num_kv_heads, int head_dim, float k_scale, float v_scale,
-                                                          __half *__restrict__ k_out, __half *__restrict__ v_out,
-                                                          int32_t *err_flag)
+// binary32 rounding.  A lane owns 8 channels, a warp whole heads of one token's
+// K and then V, kIter groups of them loaded before any is stored.
+template <int D>
+__global__ void __launch_bounds__(kRopeThreads) gather_e2m1_kernel(const uint8_t *__restrict__ k_cache,
+                                                                   const uint8_t *__restrict__ v_cache, int64_t num_pages,
+                                                                   const int32_t *__restrict__ slots, int num_tokens,
+                                                                   int num_kv_heads, float k_scale, float v_scale,
+                                                                   __half *__restrict__ k_out, __half *__restrict__ v_out,
+                                                                   int32_t *err_flag)
 {
+    constexpr int lanes = D / 8, hpw = 32 / lanes;
     grid_dependency_wait();   // the preceding kernel may write the pools
     launch_dependents();
-    const int64_t j = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (j >= num_vecs) return;
-    const bool is_v = blockIdx.y != 0;
-    const int vph = head_dim / 8;
-    const int64_t row = j / vph;                       // (token, kv head)
-    const int vec = (int)(j - row * vph);
-    const int64_t token = row / num_kv_heads;
-    const int g = (int)(row - token * num_kv_heads);
+    const int lane = threadIdx.x & 31;
+    const int64_t token = (int64_t)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
+    if (token >= num_tokens) return;
+    const int sub = lane / lanes, vec = lane % lanes;
     const int32_t slot = __ldg(slots + token);
     const int64_t page = slot >> 2;
-    float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (slot >= 0 && page < num_pages) {
-        const uint8_t *src = (is_v ? v_cache : k_cache) + (page * num_kv_heads + g) * e2m1_page_bytes(head_dim);
-        const uint32_t code = *reinterpret_cast<const uint32_t *>(src + (slot & 3) * (head_dim / 2) + vec * 4);
-        const uint32_t b = src[e2m1_scale_off(head_dim) + (vec / 2) * 4 + (slot & 3)];
-        const float block = e4m3_value(b), scale = is_v ? v_scale : k_scale;
-        const uint32_t h[4] = {e2m1_pair<0>(code), e2m1_pair<1>(code), e2m1_pair<2>(code), e2m1_pair<3>(code)};
+    const bool held = slot >= 0 && page < num_pages;      // the same on every lane
+    if (slot >= 0 && !held && lane == 0 && blockIdx.y == 0) report(err_flag, KVQ_DEV_BAD_SLOT);
+    const int groups = (num_kv_heads + hpw - 1) / hpw;    // groups of key heads, and of value heads
+    const int g0 = blockIdx.y * kIter;
+    uint32_t code[kIter];
+    uint32_t scale[kIter];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
-            y[2 * i] = __fmul_rn(__fmul_rn(f.x, block), scale);
-            y[2 * i + 1] = __fmul_rn(__fmul_rn(f.y, block), scale);
+    for (int i = 0; i < kIter; ++i) {
+        const bool is_v = g0 + i >= groups;
+        const int h = (is_v ? g0 + i - groups : g0 + i) * hpw + sub;
+        code[i] = scale[i] = 0u;
+        if (held && h < num_kv_heads) {
+            const uint8_t *src = (is_v ? v_cache : k_cache) + (page * num_kv_heads + h) * e2m1_page_bytes(D);
+            code[i] = __ldg(reinterpret_cast<const uint32_t *>(src + (slot & 3) * (D / 2)) + vec);
+            scale[i] = __ldg(src + e2m1_scale_off(D) + (vec / 2) * 4 + (slot & 3));
         }
-    } else if (slot >= 0 && g == 0 && vec == 0 && !is_v) {
-        report(err_flag, KVQ_DEV_BAD_SLOT);
     }
-    *reinterpret_cast<uint4 *>((is_v ? v_out : k_out) + row * head_dim + vec * 8) = pack8(y);
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) {
+        const bool is_v = g0 + i >= groups;
+        const int h = (is_v ? g0 + i - groups : g0 + i) * hpw + sub;
+        if (h >= num_kv_heads) continue;                  // (a group past the last value head as well)
+        const float block = e4m3_value(scale[i]), layer = is_v ? v_scale : k_scale;
+        const uint32_t p[4] = {e2m1_pair<0>(code[i]), e2m1_pair<1>(code[i]), e2m1_pair<2>(code[i]), e2m1_pair<3>(code[i])};
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&p[j]));
+            y[2 * j] = __fmul_rn(__fmul_rn(f.x, block), layer);
+            y[2 * j + 1] = __fmul_rn(__fmul_rn(f.y, block), layer);
+        }
+        *reinterpret_cast<uint4 *>((is_v ? v_out : k_out) + (token * num_kv_heads + h) * D + vec * 8) = pack8(y);
+    }
+}
+
+template <int D>
+static cudaError_t launch_gather_dim(const void *k_cache, const void *v_cache, int64_t num_pages, const int32_t *slots,
+                                     int32_t num_tokens, int32_t num_kv_heads, float k_scale, float v_scale, void *k_out,
+                                     void *v_out, int32_t *err_flag, cudaStream_t stream)
+{
+    constexpr int hpw = 32 / (D / 8);
+    const int groups = 2 * ((num_kv_heads + hpw - 1) / hpw);
+    const dim3 grid((unsigned)((num_tokens + kRopeThreads / 32 - 1) / (kRopeThreads / 32)), (unsigned)((groups + kIter - 1) / kIter));
+    if (grid.y > 65535u) return cudaErrorInvalidConfiguration;
+    return launch_pdl(gather_e2m1_kernel<D>, grid, dim3(kRopeThreads), 0, stream, static_cast<const uint8_t *>(k_cache),
+                      static_cast<const uint8_t *>(v_cache), num_pages, slots, num_tokens, num_kv_heads, k_scale, v_scale,
+                      static_cast<__half *>(k_out), static_cast<__half *>(v_out), err_flag);
 }
 
 cudaError_t launch_gather_e2m1(const void *k_cache, const void *v_cache, int64_t num_pages, const int32_t *slots,
                                int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim, float k_scale, float v_scale,
                                void *k_out, void *v_out, int32_t *err_flag, cudaStream_t stream)
 {
-    const int64_t n = (int64_t)num_tokens * num_kv_heads * (head_dim / 8);
-    if (n == 0) return cudaSuccess;
-    const int64_t blocks = (n + 255) / 256;
-    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    return launch_pdl(gather_e2m1_kernel, dim3((unsigned)blocks, 2), dim3(256), 0, stream,
-                      static_cast<const uint8_t *>(k_cache), static_cast<const uint8_t *>(v_cache), num_pages, slots, n,
-                      num_kv_heads, head_dim, k_scale, v_scale, static_cast<__half *>(k_out), static_cast<__half *>(v_out),
-                      err_flag);
+    if (num_tokens == 0) return cudaSuccess;
+    return head_dim == 128 ? launch_gather_dim<128>(k_cache, v_cache, num_pages, slots, num_tokens, num_kv_heads, k_scale,
+                                                    v_scale, k_out, v_out, err_flag, stream)
+                           : launch_gather_dim<64>(k_cache, v_cache, num_pages, slots, num_tokens, num_kv_heads, k_scale,
+                                                   v_scale, k_out, v_out, err_flag, stream);
 }
 
 // ---------------------------------------------------------------------------
