@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(32 * W, ctas_per_sm<NT, W>()) attn_e2m1_kernel
     using KF = KFrag<D>;
     using VF = VFrag<D>;
     using R = Ring<D, NT>;
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ __align__(128) uint8_t smem[];
 
     const int s = blockIdx.x, g = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -698,6 +698,8 @@ cudaError_t launch_attention_e2m1(int head_dim, const AttnArgs &a, cudaStream_t 
     // at its end for the other splits of its (sequence, kv head), which finish at about the same time,
     // instead of a second kernel that waits for all (B 32 x 4096: 21.8 -> 20.4 us).  On a grid of several
     // waves it would hold a slot that the next wave needs (B 32 x 8192, 32 rows: 91 -> 106 us).
+    // many query rows: the tcgen05 kernel
+    if (head_dim == 128 && a.rows > 8 && !a.topk_idx) return launch_attention_e2m1_tc(a, stream);
     const int64_t ctas = int64_t(a.batch) * a.num_kv_heads * a.num_splits;
     if (a.out && a.num_splits <= 8 && ctas <= e2m1_resident(a.rows)) {
         *merged = true;

@@ -116,6 +116,8 @@ cudaError_t launch_append_step(bool e4m3, int head_dim, const AttnArgs &a, cudaS
 bool tc_supported(int head_dim, int rows);
 // split-K attention over E2M1 pools (kvq_attn_e2m1.cu); *merged as for launch_attention
 cudaError_t launch_attention_e2m1(int head_dim, const AttnArgs &a, cudaStream_t stream, bool *merged);
+// its kernel for 8 < rows <= 64 at head_dim 128 without a top-k list (kvq_attn_e2m1_tc.cu): partials only
+cudaError_t launch_attention_e2m1_tc(const AttnArgs &a, cudaStream_t stream);
 // the splits a full E2M1 call uses where the caller leaves the number open and the library's rule gives
 // `most`: of 8 (or most / 4) to most, those that fill whole waves of resident CTAs, at about 1 % of the
 // time each for the merge; up to 8 stay as they are, since a batch of varied lengths balances by them
