@@ -63,6 +63,23 @@ struct VtLayout {
     static constexpr int kCols = 128 + 3 * NR <= 256 ? 256 : 512;
 };
 
+// mbar_wait_bounded that reads no clock before the barrier has been tried some times
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int *abort, int32_t *err_flag)
+{
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait_bounded(bar, parity, abort, err_flag);
+}
+
+// one lane of a converged warp
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -190,42 +207,53 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
     const uint32_t tmem = *tmem_slot;
 
     if (warp == kVtMma) {
-        // ================= MMA issue (one thread) =================
-        if (lane == 0 && ntiles > 0) {
-            const uint32_t q_addr = smem_u32(smem + T::kQ), v_addr = smem_u32(smem + T::kV), p_addr = smem_u32(smem + T::kP);
+        // ================= MMA issue =================
+        // The whole warp walks the tiles and one elected lane issues: addresses and descriptors then stay
+        // warp-uniform, and an MMA costs its 17 (A in tensor memory) or 41 cycles (A in shared memory) instead
+        // of about 46 to 85 from a branch on the lane.
+        if (ntiles > 0) {
+            const bool one = elect_one();
             const uint32_t id_qk = umma_idesc_f16(kVtTile, NR, false, false);
             const uint32_t id_pv = umma_idesc_f16(kVtTile, NR, true, true);
-            const uint64_t dq = umma_desc(q_addr, 128, (D / 8) * 128), dp = umma_desc(p_addr, NR * 16, 128);
+            const uint64_t dq = umma_desc(smem_u32(smem + T::kQ), 128, (D / 8) * 128);
+            const uint64_t dv0 = umma_desc(smem_u32(smem + T::kV), (D / 8) * 128, 128);
+            const uint64_t dp = umma_desc(smem_u32(smem + T::kP), NR * 16, 128);
             // S^T[tok][row] = sum_d K[tok][d] Q[row][d]
             auto scores = [&](int t) {
                 const int x = t & 1;
-                if (!mbar_wait_bounded(k_full(x), (t >> 1) & 1, abort_flag, a.err_flag)) return false;
+                if (!__all_sync(kFull, wait_for(k_full(x), (t >> 1) & 1, abort_flag, a.err_flag))) return false;
                 tc_fence_after();
+                if (one) {
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-                    umma_tmem_a(tmem + T::kColS + x * NR, tmem + T::kColK + x * 64 + ks * 8, dq + (uint64_t)(ks * 16), id_qk,
-                                ks > 0);
-                umma_commit(s_full(x));
-                umma_commit(k_empty(x));
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        umma_tmem_a(tmem + T::kColS + x * NR, tmem + T::kColK + x * 64 + ks * 8, dq + (uint64_t)(ks * 16), id_qk,
+                                    ks > 0);
+                    umma_commit(s_full(x));
+                    umma_commit(k_empty(x));
+                }
+                __syncwarp();
                 return true;
             };
             bool ok = scores(0);
             for (int t = 0; ok && t < ntiles; ++t) {
                 const int x = t & 1;
                 if (t + 1 < ntiles && !scores(t + 1)) break;
-                if (!mbar_wait_bounded(v_full(x), (t >> 1) & 1, abort_flag, a.err_flag)) break;
-                if (!mbar_wait_bounded(p_full, t & 1, abort_flag, a.err_flag)) break;
+                if (!__all_sync(kFull, wait_for(v_full(x), (t >> 1) & 1, abort_flag, a.err_flag))) break;
+                if (!__all_sync(kFull, wait_for(p_full, t & 1, abort_flag, a.err_flag))) break;
                 tc_fence_after();
                 // O^T[ch][row] += sum_tok V[tok][ch] P[tok][row], both MN-major
-                const uint64_t dv = umma_desc(v_addr + x * kVtTile * D * 2, (D / 8) * 128, 128);
+                const uint64_t dv = dv0 + (uint64_t)(x * (kVtTile * D * 2 / 16));
+                if (one) {
 #pragma unroll
-                for (int ks = 0; ks < kVtTile / 16; ++ks)
-                    umma_smem_a(tmem + T::kColO, dv + (uint64_t)(ks * 2 * (D / 8) * 8), dp + (uint64_t)(ks * 2 * NR), id_pv,
-                                t > 0 || ks > 0);
-                umma_commit(v_empty(x));
+                    for (int ks = 0; ks < kVtTile / 16; ++ks)
+                        umma_smem_a(tmem + T::kColO, dv + (uint64_t)(ks * 2 * (D / 8) * 8), dp + (uint64_t)(ks * 2 * NR), id_pv,
+                                    t > 0 || ks > 0);
+                    umma_commit(v_empty(x));
+                }
+                __syncwarp();
             }
             // every MMA issued so far completes before the tensor memory is freed
-            umma_commit(b_drain);
+            if (one) umma_commit(b_drain);
             mbar_wait_bounded(b_drain, 0, nullptr, a.err_flag, 100000000ull);
         }
         __syncwarp();
@@ -289,7 +317,7 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
             __syncwarp();
             if (more) fetch(kpool, rawk_s, nxt);
             else commit_copies();
-            if (t >= 2 && !__all_sync(kFull, mbar_wait_bounded(k_empty(x), ((t >> 1) - 1) & 1, abort_flag, a.err_flag))) {
+            if (t >= 2 && !__all_sync(kFull, wait_for(k_empty(x), ((t >> 1) - 1) & 1, abort_flag, a.err_flag))) {
                 ok = false;
                 break;
             }
@@ -317,7 +345,7 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
             __syncwarp();
             if (more) fetch(vpool, rawv_s, nxt);
             else commit_copies();
-            if (t >= 2 && !__all_sync(kFull, mbar_wait_bounded(v_empty(x), ((t >> 1) - 1) & 1, abort_flag, a.err_flag))) {
+            if (t >= 2 && !__all_sync(kFull, wait_for(v_empty(x), ((t >> 1) - 1) & 1, abort_flag, a.err_flag))) {
                 ok = false;
                 break;
             }
@@ -366,7 +394,7 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
             const int x = t & 1;
             const unsigned have = __ballot_sync(kFull, (unsigned)page < num_pages);   // tokens with a page
             page = token_page(t + 1);
-            ok = ok && __all_sync(kFull, mbar_wait_bounded(s_full(x), (t >> 1) & 1, abort_flag, a.err_flag));
+            ok = ok && __all_sync(kFull, wait_for(s_full(x), (t >> 1) & 1, abort_flag, a.err_flag));
             tc_fence_after();
             float2 z[NR / 2];
 #pragma unroll
@@ -456,7 +484,7 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
                     l2[r].x *= corr[2 * r];
                     l2[r].y *= corr[2 * r + 1];
                 }
-                if (t > 0) ok = ok && __all_sync(kFull, mbar_wait_bounded(v_empty((t - 1) & 1), ((t - 1) >> 1) & 1, abort_flag, a.err_flag));
+                if (t > 0) ok = ok && __all_sync(kFull, wait_for(v_empty((t - 1) & 1), ((t - 1) >> 1) & 1, abort_flag, a.err_flag));
                 tc_fence_after();
                 if (t > 0) {
 #pragma unroll
@@ -475,7 +503,7 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
             }
             // P = 2^z; P^T: (row, tok) at (tok/8) * NR*16 + (row/8) * 128 + (tok%8) * 16.  The previous tile's
             // P V has read it.
-            if (t > 0) ok = ok && __all_sync(kFull, mbar_wait_bounded(v_empty((t - 1) & 1), ((t - 1) >> 1) & 1, abort_flag, a.err_flag));
+            if (t > 0) ok = ok && __all_sync(kFull, wait_for(v_empty((t - 1) & 1), ((t - 1) >> 1) & 1, abort_flag, a.err_flag));
             uint8_t *dst = smem + T::kP + (tt >> 3) * (NR * 16) + (tt & 7) * 16;
 #pragma unroll
             for (int c = 0; c < NR / 8; ++c) {
@@ -504,7 +532,7 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
             if (32 * h + lane < NR) wmax[q * NR + 32 * h + lane] = l;
         }
         if (ok && ntiles > 0)
-            ok = __all_sync(kFull, mbar_wait_bounded(v_empty((ntiles - 1) & 1), ((ntiles - 1) >> 1) & 1, abort_flag, a.err_flag));
+            ok = __all_sync(kFull, wait_for(v_empty((ntiles - 1) & 1), ((ntiles - 1) >> 1) & 1, abort_flag, a.err_flag));
         if (!named_bar_or(1, 128, !ok)) {
             tc_fence_after();
             const int S = a.num_splits;
