@@ -173,7 +173,8 @@ static int run_attention(const AttnCall &c, bool with_combine)
     if (!c.workspace || c.workspace_bytes < workspace_layout(rows_total, S, p.head_dim).total) return KVQ_ERR_WORKSPACE;
     // the E2M1 kernel's own choice, at most the number the workspace was sized for
     if (c.e2m1 && with_combine && p.num_splits == 0 && p.split_pages == 0)
-        S = e2m1_splits(p.batch, p.num_kv_heads, int(p.num_q_heads / p.num_kv_heads) * p.q_len, S);
+        S = e2m1_splits(p.head_dim, c.topk_idx != nullptr, p.batch, p.num_kv_heads,
+                        int(p.num_q_heads / p.num_kv_heads) * p.q_len, p.max_pages_per_seq, S);
     const WorkspaceLayout wl = workspace_layout(rows_total, S, p.head_dim);
     if (p.batch == 0) return KVQ_OK;
 

@@ -22,6 +22,7 @@
 // The order of channels and tokens inside a product is free as long as both
 // operands share it: Q is loaded, and O stored, in this order.
 #include <cfloat>
+#include <cmath>
 
 #include "kvq_attn_kernel.cuh"
 #include "kvq_e2m1.cuh"
@@ -293,7 +294,11 @@ __global__ void __launch_bounds__(32 * W, ctas_per_sm<NT, W>()) attn_e2m1_kernel
     const bool early = a.early_pages && a.topk_idx == nullptr;
     if (!early) grid_dependency_wait();
     launch_dependents();
-    const SeqPick pick = seq_identity(a, blockIdx.z);
+    // On a grid of several waves the sequences come longest first, so that the short ones fill its end.
+    SeqPick pick = seq_identity(a, blockIdx.z);
+    if (!MERGE && a.longest_first) {   // (MERGE: one wave)
+        if (!__syncthreads_and(lpt_classify(a, smem, W * R::kBytes))) pick = lpt_pick(a, blockIdx.z, smem);
+    }
     const int b = pick.b;
     const SplitRange sr = split_range(a, s, b, pick.L, pick.topk_len);
     const int L = sr.L, item0 = sr.item0, item1 = sr.item1;
@@ -674,9 +679,30 @@ static cudaError_t launch_e2m1_rows(const AttnArgs &a, cudaStream_t stream)
     return launch_e2m1_width<D, 4, 2, MERGE>(a, stream);
 }
 
-int32_t e2m1_splits(int32_t batch, int32_t num_kv_heads, int rows, int32_t most)
+// whether a call runs on the tcgen05 kernel.  At 16 rows the mma.sync kernel is as fast on ragged batches and
+// faster on even ones (32 x 8192: 53 against 59 us); at 32 rows 89 against 76, ragged 210 against 154.
+static bool e2m1_uses_tc(int head_dim, int rows, bool topk) { return head_dim == 128 && rows > 16 && !topk; }
+
+int32_t e2m1_splits(int head_dim, bool topk, int32_t batch, int32_t num_kv_heads, int rows, int32_t max_pages, int32_t most)
 {
-    const int64_t pairs = int64_t(batch) * num_kv_heads, resident = e2m1_resident(rows);
+    const int64_t pairs = int64_t(batch) * num_kv_heads;
+    if (e2m1_uses_tc(head_dim, rows, topk)) {
+        // A CTA costs about 8 us beside 2 us per tile of 128 tokens (two CTAs per SM), which for full
+        // sequences gives waves * (tiles / splits * 2 + 8); of the numbers within a tenth of the least, the
+        // largest, which balances varied lengths best.
+        const int64_t resident = int64_t(device_sm_count()) * (rows <= 32 ? 2 : 1);
+        const double tiles = (max_pages + 31) / 32;
+        auto cost = [&](int32_t s) {
+            return double((pairs * s + resident - 1) / resident) * (std::ceil(tiles / s) * 2.0 + 8.0);
+        };
+        double least = cost(1);
+        for (int32_t s = 2; s <= most; ++s) least = std::fmin(least, cost(s));
+        int32_t s = most;
+        while (s > 1 && cost(s) > 1.1 * least) --s;
+        return s;
+    }
+    if (topk) return most;   // lists and whole contexts side by side: varied work again
+    const int64_t resident = e2m1_resident(rows);
     int32_t best = most;
     double score = 0.0;
     for (int32_t s = most / 4 > 8 ? most / 4 : 8; s <= most; ++s) {
@@ -690,7 +716,7 @@ int32_t e2m1_splits(int32_t batch, int32_t num_kv_heads, int rows, int32_t most)
     return best;
 }
 
-cudaError_t launch_attention_e2m1(int head_dim, const AttnArgs &a, cudaStream_t stream, bool *merged)
+cudaError_t launch_attention_e2m1(int head_dim, AttnArgs a, cudaStream_t stream, bool *merged)
 {
     *merged = false;
     if (a.batch == 0) return cudaSuccess;
@@ -698,9 +724,10 @@ cudaError_t launch_attention_e2m1(int head_dim, const AttnArgs &a, cudaStream_t 
     // at its end for the other splits of its (sequence, kv head), which finish at about the same time,
     // instead of a second kernel that waits for all (B 32 x 4096: 21.8 -> 20.4 us).  On a grid of several
     // waves it would hold a slot that the next wave needs (B 32 x 8192, 32 rows: 91 -> 106 us).
-    // many query rows: the tcgen05 kernel
-    if (head_dim == 128 && a.rows > 8 && !a.topk_idx) return launch_attention_e2m1_tc(a, stream);
+    if (e2m1_uses_tc(head_dim, a.rows, a.topk_idx != nullptr)) return launch_attention_e2m1_tc(a, stream);
     const int64_t ctas = int64_t(a.batch) * a.num_kv_heads * a.num_splits;
+    // (B 64, 1K to 32K: 109 -> 94 us, with 16 rows 138 -> 110; B 32 x 32K, all equal: 118 -> 119)
+    a.longest_first = a.batch > 1 && ctas > e2m1_resident(a.rows);
     if (a.out && a.num_splits <= 8 && ctas <= e2m1_resident(a.rows)) {
         *merged = true;
         return head_dim == 128 ? launch_e2m1_rows<128, true>(a, stream) : launch_e2m1_rows<64, true>(a, stream);

@@ -1,5 +1,5 @@
 // kvq_attn_e2m1_tc.cu -- split-K paged attention over the 4-bit (E2M1) cache for
-// many query rows per kv head (MTP verify: G heads x q_len rows, 8 < rows <= 64,
+// many query rows per kv head (MTP verify: G heads x q_len rows, 16 < rows <= 64,
 // head_dim 128, no top-k list) on the fifth-generation tensor cores.
 //
 // The same partials as attn_e2m1_kernel, which decodes every code once per
@@ -609,7 +609,6 @@ static cudaError_t launch_vt(const AttnArgs &a, cudaStream_t stream)
 
 cudaError_t launch_attention_e2m1_tc(const AttnArgs &a, cudaStream_t stream)
 {
-    if (a.rows <= 16) return launch_vt<16>(a, stream);
     if (a.rows <= 32) return launch_vt<32>(a, stream);
     return launch_vt<64>(a, stream);
 }

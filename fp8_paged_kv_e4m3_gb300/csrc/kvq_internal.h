@@ -115,13 +115,14 @@ cudaError_t launch_attention_step(bool e4m3, int head_dim, const AttnArgs &a, cu
 cudaError_t launch_append_step(bool e4m3, int head_dim, const AttnArgs &a, cudaStream_t stream);
 bool tc_supported(int head_dim, int rows);
 // split-K attention over E2M1 pools (kvq_attn_e2m1.cu); *merged as for launch_attention
-cudaError_t launch_attention_e2m1(int head_dim, const AttnArgs &a, cudaStream_t stream, bool *merged);
-// its kernel for 8 < rows <= 64 at head_dim 128 without a top-k list (kvq_attn_e2m1_tc.cu): partials only
+cudaError_t launch_attention_e2m1(int head_dim, AttnArgs a, cudaStream_t stream, bool *merged);
+// its kernel for 16 < rows <= 64 at head_dim 128 without a top-k list (kvq_attn_e2m1_tc.cu): partials only
 cudaError_t launch_attention_e2m1_tc(const AttnArgs &a, cudaStream_t stream);
 // the splits a full E2M1 call uses where the caller leaves the number open and the library's rule gives
-// `most`: of 8 (or most / 4) to most, those that fill whole waves of resident CTAs, at about 1 % of the
-// time each for the merge; up to 8 stay as they are, since a batch of varied lengths balances by them
-int32_t e2m1_splits(int32_t batch, int32_t num_kv_heads, int rows, int32_t most);
+// `most`: never more, since the workspace is sized for those.  On the mma.sync kernel, of 8 (or most / 4) to
+// most, those that fill whole waves of resident CTAs, at about 1 % of the time each for the merge; up to 8
+// stay as they are, since a batch of varied lengths balances by them.
+int32_t e2m1_splits(int head_dim, bool topk, int32_t batch, int32_t num_kv_heads, int rows, int32_t max_pages, int32_t most);
 // append with rotary positions, or (rotate false) the plain append to E2M1 pools; the E2M1
 // read-back; the rotation table (kvq_rope.cu)
 cudaError_t launch_append_rope(PoolKind pool, bool rotate, RopeArgs a, cudaStream_t stream);

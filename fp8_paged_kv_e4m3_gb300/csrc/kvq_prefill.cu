@@ -77,7 +77,8 @@ constexpr int kPfBar = kPfRing + kPfStages * 2 * kPfTileBytes;
 constexpr int kPfNumBars = 2 * kPfStages + 2 + 2 + 2 + 2 + 2 + 1;
 constexpr int kPfAbort = kPfBar + 8 * kPfNumBars;
 constexpr int kPfTmemSlot = kPfAbort + 8;
-constexpr int kPfSmemBytes = kPfTmemSlot + 8;
+constexpr int kPfCount = kPfTmemSlot + 8;           // the sorted pairs: count, then the entries
+constexpr int kPfSmemBytes = kPfCount + 16 + 512 * 4;
 static_assert(kPfSmemBytes <= 232448, "prefill shared memory exceeds one CTA's limit");
 
 // tensor-memory columns: S_A, S_B (P written over the first 64 columns of the
@@ -188,18 +189,41 @@ __global__ void __launch_bounds__(256) kv_tile_kernel(const PrefillArgs a)
 // 2. flash attention over the tiles
 
 // Work items: (sequence b, query head h, pair of query tiles), longest first.
-// Item i has rank r = i / (B Hq) from the top (pair = pairs(b) - 1 - r), and
-// b = (i % (B Hq)) % B, h = (i % (B Hq)) / B.  An item whose sequence has
-// fewer pairs, or is not a valid chunk, is empty (pair < 0).  Each CTA takes
-// its items in rounds of gridDim.x, in alternating direction, so that the
-// CTAs' shares of the descending sizes even out.
+// With several sequences of up to kPfSorted pairs in all, the pairs are sorted
+// by the key tiles they attend (a chunk's history counts), by each CTA in its
+// prologue, and item i is head i % Hq of sorted pair i / Hq.  Otherwise (one
+// sequence: the same order) item i has rank r = i / (B Hq) from the top
+// (pair = pairs(b) - 1 - r), and b = (i % (B Hq)) % B, h = (i % (B Hq)) / B.
+// An item whose sequence has fewer pairs, or is not a valid chunk, is empty
+// (pair < 0).  Each CTA takes its items in rounds of gridDim.x, in alternating
+// direction, so that the CTAs' shares of the descending sizes even out.  The
+// order changes no result.
 struct PfItem {
     int b, h, pair, q0, n, L;
 };
 
-__device__ __forceinline__ PfItem pf_item(const PrefillArgs &a, int i)
+constexpr int kPfSorted = 512, kPfSortedBatch = 64;
+// the sorted pairs in shared memory: count (0: not used), then b << 16 | pair
+struct PfOrder {
+    const volatile int *count;
+    const int *entry;
+};
+
+__device__ __forceinline__ PfItem pf_item(const PrefillArgs &a, const PfOrder &ord, int i)
 {
     PfItem it;
+    const int sorted = *ord.count;
+    if (sorted > 0) {
+        const int e = i / a.num_q_heads;
+        it.h = i - e * a.num_q_heads;
+        const int w = e < sorted ? ord.entry[e] : 0;
+        it.b = w >> 16;
+        it.pair = e < sorted ? (w & 0xFFFF) : -1;
+        it.q0 = __ldg(a.q_start + it.b);
+        it.n = __ldg(a.q_start + it.b + 1) - it.q0;
+        it.L = __ldg(a.context_lens + it.b);
+        return it;
+    }
     const int per = a.batch * a.num_q_heads;
     const int rnk = i / per, rem = i - rnk * per;
     it.b = rem % a.batch;
@@ -226,14 +250,62 @@ __device__ __forceinline__ int pf_tiles_of(const PfItem &it, int x)
 }
 
 // this CTA's next non-empty item from position k on; false when none is left
-__device__ __forceinline__ bool pf_next(const PrefillArgs &a, int total, int &k, PfItem &it)
+__device__ __forceinline__ bool pf_next(const PrefillArgs &a, const PfOrder &ord, int total, int &k, PfItem &it)
 {
     for (;; ++k) {
         const int i = pf_item_index(k);
         if (i >= total) return false;
-        it = pf_item(a, i);
+        it = pf_item(a, ord, i);
         if (it.pair >= 0) return true;
     }
+}
+
+// Fills the order (by the whole CTA); `scratch`: kPfSorted + kPfSortedBatch + 1 ints.  Reads the lengths,
+// which the tile gather does not write.
+__device__ __forceinline__ void pf_sort(const PrefillArgs &a, volatile int *count, int *entry, int *scratch)
+{
+    int *cost = scratch, *first = scratch + kPfSorted;   // first[b]: pairs of the sequences before b
+    const int B = a.batch;
+    if (B < 2 || B > kPfSortedBatch) {
+        if (threadIdx.x == 0) *count = 0;
+        __syncthreads();
+        return;
+    }
+    for (int b = threadIdx.x; b < B; b += kPfThreads) {
+        const int q0 = __ldg(a.q_start + b), q1 = __ldg(a.q_start + b + 1);
+        first[b + 1] = seq_ok(a, q0, q1, __ldg(a.context_lens + b)) ? (q1 - q0 + 2 * kPfTile - 1) / (2 * kPfTile) : 0;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        int sum = 0;
+        first[0] = 0;
+        for (int b = 1; b <= B; ++b) {
+            sum = min(sum + first[b], kPfSorted + 1);     // (each term is at most 2^31 / 256)
+            first[b] = sum;
+        }
+        *count = sum <= kPfSorted ? sum : 0;
+    }
+    __syncthreads();
+    const int n = *count;
+    for (int e = threadIdx.x; e < n; e += kPfThreads) {
+        int b = 0;
+        while (first[b + 1] <= e) ++b;
+        PfItem it;
+        it.pair = e - first[b];
+        it.q0 = __ldg(a.q_start + b);
+        it.n = __ldg(a.q_start + b + 1) - it.q0;
+        it.L = __ldg(a.context_lens + b);
+        cost[e] = max(pf_tiles_of(it, 0), pf_tiles_of(it, 1));
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < n; e += kPfThreads) {
+        int rank = 0, b = 0;
+        for (int j = 0; j < n; ++j) rank += cost[j] > cost[e] || (cost[j] == cost[e] && j < e);
+        while (first[b + 1] <= e) ++b;
+        entry[rank] = (b << 16) | (e - first[b]);
+    }
+    fence_async_smem();   // bulk copies overwrite the scratch
+    __syncthreads();
 }
 
 template <bool E4M3>
@@ -242,6 +314,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attn_kernel(const Prefi
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int total = ((a.max_q_len + 2 * kPfTile - 1) / (2 * kPfTile)) * a.batch * a.num_q_heads;
+    const PfOrder ord = {reinterpret_cast<volatile int *>(smem + kPfCount), reinterpret_cast<const int *>(smem + kPfCount + 16)};
+    pf_sort(a, reinterpret_cast<volatile int *>(smem + kPfCount), reinterpret_cast<int *>(smem + kPfCount + 16),
+            reinterpret_cast<int *>(smem + kPfRing));   // (the ring is not in use yet)
 
     // chunks that cannot be attended are flagged once per launch
     // (q_start and context_lens are read before grid_dependency_wait: the
@@ -295,7 +370,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attn_kernel(const Prefi
             const uint64_t pol = l2_policy_evict_last();   // every query tile of the group re-reads them
             bool ok = true;
             PfItem it;
-            for (int k = 0; ok && pf_next(a, total, k, it); ++k) {
+            for (int k = 0; ok && pf_next(a, ord, total, k, it); ++k) {
                 const int ntiles = max(pf_tiles_of(it, 0), pf_tiles_of(it, 1));
                 const uint8_t *src =
                     a.tiles + (((int64_t)it.b * a.num_kv_heads + it.h / a.group) * a.max_tiles) * 2 * kPfTileBytes;
@@ -355,7 +430,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attn_kernel(const Prefi
             int T0 = 0, ni = 0, np[2] = {0, 0};   // tiles before this item, items, P waits per tile
             bool ok = true;
             PfItem it;
-            for (int k = 0; ok && pf_next(a, total, k, it); ++k, ++ni) {
+            for (int k = 0; ok && pf_next(a, ord, total, k, it); ++k, ++ni) {
                 const int nt_a = pf_tiles_of(it, 0), nt_b = pf_tiles_of(it, 1);
                 const int ntiles = max(nt_a, nt_b);
                 // both query tiles of the item in shared memory; their groups may then write the next item's
@@ -431,7 +506,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attn_kernel(const Prefi
         int k = 0, ni = 0, ns = 0, npv = 0;   // item position, items, S waits and P V commits of tile X so far
         bool ok = true;                       // the same on every lane: tensor-memory loads and stores are warp-wide
         PfItem it;
-        bool have = pf_next(a, total, k, it);
+        bool have = pf_next(a, ord, total, k, it);
         if (have) load_q(it);
         while (have && ok) {
             const int h = it.h, g = h / a.group, q0 = it.q0, n = it.n;
@@ -544,7 +619,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attn_kernel(const Prefi
             // thread has taken this item's Q (so that no Q arrival runs two items ahead)
             ++k;
             PfItem nxt;
-            const bool have_next = ok && pf_next(a, total, k, nxt);
+            const bool have_next = ok && pf_next(a, ord, total, k, nxt);
             if (have_next) {
                 if (!__all_sync(kPfFull, mbar_wait_bounded(b_qf, ni & 1, abort_flag, a.err_flag))) ok = false;
                 else load_q(nxt);

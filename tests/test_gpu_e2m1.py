@@ -365,24 +365,26 @@ def test_decode_rows_that_a_mask_leaves_empty():
         E.close(out, ref, tol)
 
 
-def test_decode_nan_scale_inside_the_context_reaches_its_rows_alone():
-    q, kc, vc, bt, lens, ks, vs, _, _ = _problem(14, 2, 1, 8, 2, 128, [150, 150])
+@pytest.mark.parametrize("q_len,Hq", [(1, 8), (4, 16), (4, 32)])
+def test_decode_nan_scale_inside_the_context_reaches_its_rows_alone(q_len, Hq):
+    q, kc, vc, bt, lens, ks, vs, _, _ = _problem(14, 2, q_len, Hq, 2, 128, [150, 150])
     for pool in (kc, vc):
         bad = pool.copy()
         bad[bt[0, 20], 1, 256 + 4 * 3 + 2] = 0x7F        # sequence 0, kv head 1, token 82, block 3
         pools = (bad, vc) if pool is kc else (kc, bad)
         out, err = _run(q, *pools, bt, lens, ks, vs, None, None, num_splits=4)
         ref, tol, _ = E.decode(q, kc, vc, bt, lens, ks, vs)
-        rows = np.isnan(out[0, 0, 4:])
-        assert rows.all() if pool is kc else (rows[:, 48:64].all() and not rows[:, :48].any())
+        rows = np.isnan(out[0, :, Hq // 2:])
+        assert rows.all() if pool is kc else (rows[..., 48:64].all() and not rows[..., :48].any())
         E.close(out[1], ref[1], tol[1])
-        E.close(out[0, :, :4], ref[0, :, :4], tol[0, :, :4])
+        E.close(out[0, :, :Hq // 2], ref[0, :, :Hq // 2], tol[0, :, :Hq // 2])
 
 
-def test_decode_large_scores_and_rising_maxima():
+@pytest.mark.parametrize("q_len,Hq,Hkv", [(1, 4, 1), (4, 4, 1), (4, 8, 1), (3, 8, 1), (4, 12, 1)])
+def test_decode_large_scores_and_rising_maxima(q_len, Hq, Hkv):
     """Scores in ascending order over hundreds of units (the running maximum moves all the time), and a temperature."""
-    q, kc, vc, bt, lens, ks, vs, _, _ = _problem(15, 1, 1, 4, 1, 128, [777])
-    rows = np.linspace(0.01, 30, 777)[:, None, None] * np.ones((777, 1, 128))
+    q, kc, vc, bt, lens, ks, vs, _, _ = _problem(15, 1, q_len, Hq, Hkv, 128, [777])
+    rows = np.linspace(0.01, 30, 777)[:, None, None] * np.ones((777, Hkv, 128))
     slots = bt[0, np.arange(777) // 4] * 4 + np.arange(777) % 4
     kc = E.append(kc, rows.astype(np.float32), slots, ks)
     q[:] = np.abs(q)
@@ -390,6 +392,36 @@ def test_decode_large_scores_and_rising_maxima():
         out, _ = _run(q, kc, vc, bt, lens, ks, vs, None, None, num_splits=2, sm_scale=sm or 0.0)
         ref, tol, _ = E.decode(q, kc, vc, bt, lens, ks, vs, sm=sm)
         E.close(out, ref, tol)
+    # and in descending order, negated queries: every score below the first ones by far more than fp16 reaches
+    out, _ = _run(-q, kc, vc, bt, lens, ks, vs, None, None, num_splits=2)
+    ref, tol, _ = E.decode(-q, kc, vc, bt, lens, ks, vs)
+    E.close(out, ref, tol)
+
+
+@pytest.mark.parametrize("q_len,Hq,Hkv", [(2, 8, 2), (4, 8, 1), (4, 16, 1), (3, 16, 2)])
+@pytest.mark.parametrize("splits", [1, 4])
+def test_decode_dense_bad_pages(q_len, Hq, Hkv, splits):
+    q, kc, vc, bt, lens, ks, vs, _, _ = _problem(22, 3, q_len, Hq, Hkv, 128, [500, 140, 260])
+    bt[0, 3], bt[0, 70], bt[0, 124], bt[1, 0], bt[2, 64] = -1, kc.shape[0], 2 ** 31 - 1, -5, -2 ** 31
+    out, err = _run(q, kc, vc, bt, lens, ks, vs, None, None, num_splits=splits)
+    ref, tol, flags = E.decode(q, kc, vc, bt, lens, ks, vs)
+    assert err == flags == kvq.DEV_BAD_PAGE
+    E.close(out, ref, tol)
+
+
+@pytest.mark.parametrize("q_len,Hq,D,topk", [(1, 8, 128, None), (1, 8, 64, 30), (4, 16, 128, None), (4, 32, 128, None)])
+def test_decode_longest_first_over_several_waves(q_len, Hq, D, topk):
+    """More CTAs than the card holds at once, lengths from 4 to 300: the sequences are taken longest first."""
+    lens = [4 + (97 * i) % 297 for i in range(300)]
+    pr = _problem(23, 300, q_len, Hq, 2, D, lens, topk=topk)
+    out, err = _run(*pr, num_splits=3)
+    q, kc, vc, bt, lens, ks, vs, idx, counts = pr
+    some = np.r_[0:300:37, 299]                          # the reference takes a few of them
+    cut = lambda x: None if x is None else x[some]  # noqa: E731
+    ref, tol, flags = E.decode(q[some], kc, vc, bt[some], lens[some], ks, vs, cut(idx), cut(counts))
+    assert err == flags == 0
+    E.close(out[some], ref, tol)
+    assert np.isfinite(out).all() and (np.abs(out).max((1, 2, 3)) > 0).all()
 
 
 def test_decode_is_deterministic_and_partials_combine_to_it():
