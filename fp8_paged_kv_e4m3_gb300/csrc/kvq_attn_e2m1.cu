@@ -267,10 +267,10 @@ __device__ __forceinline__ void softmax_unit(const float (&sc)[NT][kUnitTiles][4
 
 // NT n-tiles of 8 query rows per warp; RW warps share the same tokens and split
 // the query rows, the W / RW groups of warps split the tokens.
-// MERGE: the splits of one (sequence, kv head) are one thread-block cluster; after
+// LISTS: the call has top-k lists (a sequence of it may have none).  MERGE: the splits of one (sequence, kv head) are one thread-block cluster; after
 // a cluster barrier its CTAs merge the partials (the combine's function, hence
 // its bits) and write the output themselves.
-template <int D, int NT, int RW, int W, bool MERGE>
+template <int D, int NT, int RW, int W, bool MERGE, bool LISTS>
 __global__ void __launch_bounds__(32 * W, ctas_per_sm<NT, W>()) attn_e2m1_kernel(const AttnArgs a)
 {
     constexpr int kQWarps = W, kQThreads = 32 * W;
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(32 * W, ctas_per_sm<NT, W>()) attn_e2m1_kernel
     // Without a top-k list, block tables, lengths and the pages of positions
     // below L - q_len may be read before the preceding kernel (the step's
     // append) has finished; everything else waits for it.
-    const bool early = a.early_pages && a.topk_idx == nullptr;
+    const bool early = !LISTS && a.early_pages;
     if (!early) grid_dependency_wait();
     launch_dependents();
     // On a grid of several waves the sequences come longest first, so that the short ones fill its end.
@@ -300,8 +300,9 @@ __global__ void __launch_bounds__(32 * W, ctas_per_sm<NT, W>()) attn_e2m1_kernel
         if (!__syncthreads_and(lpt_classify(a, smem, W * R::kBytes))) pick = lpt_pick(a, blockIdx.z, smem);
     }
     const int b = pick.b;
-    const SplitRange sr = split_range(a, s, b, pick.L, pick.topk_len);
+    const SplitRange sr = split_range(a, s, b, pick.L, LISTS ? pick.topk_len : 0);
     const int L = sr.L, item0 = sr.item0, item1 = sr.item1;
+    const bool topk = LISTS && sr.topk;
 
     // this lane's places inside a page
     const int page_stride = a.num_kv_heads * PB;   // at most 65535 * 288
@@ -348,7 +349,7 @@ __global__ void __launch_bounds__(32 * W, ctas_per_sm<NT, W>()) attn_e2m1_kernel
     };
     int pg[R::kUnits];                     // pages of the units in flight, the next one first
     bool waited = !early;
-    if (!sr.topk) {
+    if (!topk) {
 #pragma unroll
         for (int d = 0; d < R::kUnits; ++d) pg[d] = raw_page(u0 + d * step);
 #pragma unroll
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(32 * W, ctas_per_sm<NT, W>()) attn_e2m1_kernel
     if (!waited) grid_dependency_wait();
     if (threadIdx.x == 0) {
         if (!sr.len_ok) report(a.err_flag, KVQ_DEV_BAD_LEN);
-        if (sr.len_ok && pick.topk_len > a.max_topk) report(a.err_flag, KVQ_DEV_BAD_TOPK);
+        if (LISTS && sr.len_ok && pick.topk_len > a.max_topk) report(a.err_flag, KVQ_DEV_BAD_TOPK);
     }
 
     float o[NT][D / 16][4];
@@ -420,11 +421,12 @@ __global__ void __launch_bounds__(32 * W, ctas_per_sm<NT, W>()) attn_e2m1_kernel
     uint32_t pf[NT][kUnitTiles][2];
     constexpr int kNoToken = 0x7FFFFFFF;   // a position beyond every row's limit
 
-    if (!sr.topk) {
+    if (!topk) {
         const int clean_end = (L - a.q_len + 1) / 4;     // pages below hold only positions that every row sees
+        int next = raw_page(u0 + R::kUnits * step);
         for (int slot = 0; u0 < item1; u0 += step) {
             const int u = u0 + R::kUnits * step;         // the unit this slot holds next
-            const int next = raw_page(u);
+            const int ahead = raw_page(u + step);        // (the block table is read a unit before it is used)
             copy_wait<R::kUnits - 1>();
             const uint8_t *un = ring + slot * R::kUnit;
             {
@@ -475,11 +477,13 @@ __global__ void __launch_bounds__(32 * W, ctas_per_sm<NT, W>()) attn_e2m1_kernel
 #pragma unroll
             for (int d = 0; d + 1 < R::kUnits; ++d) pg[d] = pg[d + 1];
             pg[R::kUnits - 1] = checked(next, u);
+            next = ahead;
             if (u < item1) fetch(pg[R::kUnits - 1], slot);
             copy_commit();
             slot = slot + 1 == R::kUnits ? 0 : slot + 1;
         }
-    } else {
+    }
+    if constexpr (LISTS) if (topk) {
         // --- top-k: a unit is 32 list entries; entry 16 k + 4 p + j is token j of page slot p of
         // tile k; lane l holds entry l's position (-1: none) and page ---
         const int32_t *list = a.topk_idx + ((int64_t)b * a.num_kv_heads + g) * a.max_topk;
@@ -499,20 +503,6 @@ __global__ void __launch_bounds__(32 * W, ctas_per_sm<NT, W>()) attn_e2m1_kernel
                 }
             }
             const unsigned live = __ballot_sync(kFull, pos >= 0);
-            VF vf[kUnitTiles];
-#pragma unroll
-            for (int k = 0; k < kUnitTiles; ++k) {
-                vf[k].s = 0u;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int e = 16 * k + 4 * t + j;
-                    const int at = __shfl_sync(kFull, pos, e) & 3;
-                    const uint8_t *row = vpool + (int64_t)__shfl_sync(kFull, phys, e) * page_stride;
-                    load_words(vf[k].x[j], row + v_code + at * (D / 2));
-                    vf[k].s |= (uint32_t)row[v_scale + at] << (8 * j);
-                }
-                vf[k].s &= byte_mask((live >> (16 * k + 4 * t)) & 15u);
-            }
             KF kf[kUnitTiles];
             int row_pos[kUnitTiles][2];
 #pragma unroll
@@ -532,6 +522,20 @@ __global__ void __launch_bounds__(32 * W, ctas_per_sm<NT, W>()) attn_e2m1_kernel
                 }
             }
             scores<D, NT, RW>(kf, ks_sel, qs, sc);
+            VF vf[kUnitTiles];
+#pragma unroll
+            for (int k = 0; k < kUnitTiles; ++k) {
+                vf[k].s = 0u;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int e = 16 * k + 4 * t + j;
+                    const int at = __shfl_sync(kFull, pos, e) & 3;
+                    const uint8_t *row = vpool + (int64_t)__shfl_sync(kFull, phys, e) * page_stride;
+                    load_words(vf[k].x[j], row + v_code + at * (D / 2));
+                    vf[k].s |= (uint32_t)row[v_scale + at] << (8 * j);
+                }
+                vf[k].s &= byte_mask((live >> (16 * k + 4 * t)) & 15u);
+            }
 #pragma unroll
             for (int k = 0; k < kUnitTiles; ++k)
 #pragma unroll
@@ -614,7 +618,7 @@ __global__ void __launch_bounds__(32 * W, ctas_per_sm<NT, W>()) attn_e2m1_kernel
 
 // ---------------------------------------------------------------------------
 
-template <int D, int NT, int RW, int W, bool MERGE>
+template <int D, int NT, int RW, int W, bool MERGE, bool LISTS>
 static cudaError_t launch_e2m1(const AttnArgs &a, cudaStream_t stream)
 {
     constexpr int merge = W * NT * 8 * (D + 4) * 4, ring = W * Ring<D, NT>::kBytes + q_bytes<D, NT, RW>();
@@ -625,7 +629,7 @@ static cudaError_t launch_e2m1(const AttnArgs &a, cudaStream_t stream)
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 64 && !(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & (1ull << dev))) {
-        e = cudaFuncSetAttribute(attn_e2m1_kernel<D, NT, RW, W, MERGE>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        e = cudaFuncSetAttribute(attn_e2m1_kernel<D, NT, RW, W, MERGE, LISTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
         __atomic_fetch_or(&configured, 1ull << dev, __ATOMIC_ACQ_REL);
     }
@@ -643,7 +647,7 @@ static cudaError_t launch_e2m1(const AttnArgs &a, cudaStream_t stream)
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = MERGE ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, attn_e2m1_kernel<D, NT, RW, W, MERGE>, a);
+    return cudaLaunchKernelEx(&cfg, attn_e2m1_kernel<D, NT, RW, W, MERGE, LISTS>, a);
 }
 
 // The CTAs of W = 4 warps that are resident at once.
@@ -656,27 +660,27 @@ static int64_t e2m1_resident(int rows)
 
 // A grid that leaves most of the card idle takes wider CTAs: the same splits, each
 // walked by two or four times as many warps.
-template <int D, int NT, int RW, bool MERGE>
+template <int D, int NT, int RW, bool MERGE, bool LISTS>
 static cudaError_t launch_e2m1_width(const AttnArgs &a, cudaStream_t stream)
 {
     const int64_t ctas = int64_t(a.batch) * a.num_kv_heads * a.num_splits, resident = e2m1_resident(a.rows);
     // (a cluster's CTAs share a GPC: one of more than four CTAs that each fill an SM may not find room)
     if constexpr (NT == 1)
         if (MERGE ? a.num_splits <= 4 && ctas <= 128 : ctas * 4 <= resident)
-            return launch_e2m1<D, NT, RW, 16, MERGE>(a, stream);
-    if (ctas * 2 <= resident) return launch_e2m1<D, NT, RW, 8, MERGE>(a, stream);
-    return launch_e2m1<D, NT, RW, 4, MERGE>(a, stream);
+            return launch_e2m1<D, NT, RW, 16, MERGE, LISTS>(a, stream);
+    if (ctas * 2 <= resident) return launch_e2m1<D, NT, RW, 8, MERGE, LISTS>(a, stream);
+    return launch_e2m1<D, NT, RW, 4, MERGE, LISTS>(a, stream);
 }
 
-template <int D, bool MERGE>
+template <int D, bool MERGE, bool LISTS>
 static cudaError_t launch_e2m1_rows(const AttnArgs &a, cudaStream_t stream)
 {
     const int tiles = (a.rows + 7) / 8;
-    if (tiles <= 1) return launch_e2m1_width<D, 1, 1, MERGE>(a, stream);
-    if (tiles <= 2) return launch_e2m1_width<D, 2, 1, MERGE>(a, stream);
-    if (tiles <= 3) return launch_e2m1_width<D, 3, 1, MERGE>(a, stream);
-    if (tiles <= 4) return launch_e2m1_width<D, 4, 1, MERGE>(a, stream);
-    return launch_e2m1_width<D, 4, 2, MERGE>(a, stream);
+    if (tiles <= 1) return launch_e2m1_width<D, 1, 1, MERGE, LISTS>(a, stream);
+    if (tiles <= 2) return launch_e2m1_width<D, 2, 1, MERGE, LISTS>(a, stream);
+    if (tiles <= 3) return launch_e2m1_width<D, 3, 1, MERGE, LISTS>(a, stream);
+    if (tiles <= 4) return launch_e2m1_width<D, 4, 1, MERGE, LISTS>(a, stream);
+    return launch_e2m1_width<D, 4, 2, MERGE, LISTS>(a, stream);
 }
 
 // whether a call runs on the tcgen05 kernel.  At 16 rows the mma.sync kernel is as fast on ragged batches and
@@ -728,11 +732,13 @@ cudaError_t launch_attention_e2m1(int head_dim, AttnArgs a, cudaStream_t stream,
     const int64_t ctas = int64_t(a.batch) * a.num_kv_heads * a.num_splits;
     // (B 64, 1K to 32K: 109 -> 94 us, with 16 rows 138 -> 110; B 32 x 32K, all equal: 118 -> 119)
     a.longest_first = a.batch > 1 && ctas > e2m1_resident(a.rows);
-    if (a.out && a.num_splits <= 8 && ctas <= e2m1_resident(a.rows)) {
+    if (a.out && !a.topk_idx && a.num_splits <= 8 && ctas <= e2m1_resident(a.rows)) {
         *merged = true;
-        return head_dim == 128 ? launch_e2m1_rows<128, true>(a, stream) : launch_e2m1_rows<64, true>(a, stream);
+        return head_dim == 128 ? launch_e2m1_rows<128, true, false>(a, stream) : launch_e2m1_rows<64, true, false>(a, stream);
     }
-    return head_dim == 128 ? launch_e2m1_rows<128, false>(a, stream) : launch_e2m1_rows<64, false>(a, stream);
+    if (a.topk_idx)
+        return head_dim == 128 ? launch_e2m1_rows<128, false, true>(a, stream) : launch_e2m1_rows<64, false, true>(a, stream);
+    return head_dim == 128 ? launch_e2m1_rows<128, false, false>(a, stream) : launch_e2m1_rows<64, false, false>(a, stream);
 }
 
 }  // namespace kvq
