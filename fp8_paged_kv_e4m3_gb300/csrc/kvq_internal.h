@@ -116,6 +116,8 @@ cudaError_t launch_append_step(bool e4m3, int head_dim, const AttnArgs &a, cudaS
 bool tc_supported(int head_dim, int rows);
 // split-K attention over E2M1 pools (kvq_attn_e2m1.cu); *merged as for launch_attention
 cudaError_t launch_attention_e2m1(int head_dim, AttnArgs a, cudaStream_t stream, bool *merged);
+// the mma.sync kernel at head_dim 64 (kvq_attn_e2m1_d64.cu)
+cudaError_t launch_attention_e2m1_d64(const AttnArgs &a, bool merge, cudaStream_t stream);
 // its kernel for 16 < rows <= 64 at head_dim 128 without a top-k list (kvq_attn_e2m1_tc.cu): partials only
 cudaError_t launch_attention_e2m1_tc(const AttnArgs &a, cudaStream_t stream);
 // the splits a full E2M1 call uses where the caller leaves the number open and the library's rule gives
