@@ -72,14 +72,6 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile
     return mbar_wait_bounded(bar, parity, abort, err_flag);
 }
 
-// one lane of a converged warp
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
-
 __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");

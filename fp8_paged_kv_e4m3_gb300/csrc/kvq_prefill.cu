@@ -392,8 +392,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attn_kernel(const Prefi
         }
         __syncwarp();   // the whole warp reaches the teardown barrier together
     } else if (warp == kPfMmaWarp) {
-        // ================= MMA issue (one thread) =================
-        if (lane == 0) {
+        // ================= MMA issue =================
+        // The whole warp walks the items and one elected lane issues, so that addresses and descriptors stay
+        // warp-uniform (from a branch on the lane an MMA took about 100 cycles to issue, of which it needs 64).
+        {
+            const bool one = elect_one();
             const uint32_t id_qk = umma_idesc_f16(kPfTile, kPfTile, false, false);
             const uint32_t id_pv = umma_idesc_f16(kPfTile, kPfD, false, true);
             const uint32_t q_addr = smem_u32(smem + kPfQ);
@@ -406,24 +409,31 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attn_kernel(const Prefi
                 const uint32_t k_addr = smem_u32(smem + kPfRing + (T % kPfStages) * 2 * kPfTileBytes);
                 const uint64_t dq = umma_desc(q_addr + x * kPfTileBytes, 128, 2048);
                 const uint64_t dk = umma_desc(k_addr, 128, 2048);
+                if (one) {
 #pragma unroll
-                for (int ks = 0; ks < kPfD / 16; ++ks)
-                    umma_smem_a(tmem + kPfColS + x * kPfTile, dq + (uint64_t)(ks * 16), dk + (uint64_t)(ks * 16),
-                                id_qk, ks > 0);
-                umma_commit(b_s0 + 8 * x);
+                    for (int ks = 0; ks < kPfD / 16; ++ks)
+                        umma_smem_a(tmem + kPfColS + x * kPfTile, dq + (uint64_t)(ks * 16), dk + (uint64_t)(ks * 16),
+                                    id_qk, ks > 0);
+                    umma_commit(b_s0 + 8 * x);
+                }
+                __syncwarp();
             };
             // O_X (+)= P_X V_T: A = P (tensor memory, two fp16 per column), B = V (MN-major)
             auto pv = [&](int x, int T, bool acc) {
                 const uint32_t v_addr = smem_u32(smem + kPfRing + (T % kPfStages) * 2 * kPfTileBytes + kPfTileBytes);
                 const uint64_t dv = umma_desc(v_addr, 2048, 128);
+                if (one) {
 #pragma unroll
-                for (int ks = 0; ks < kPfTile / 16; ++ks)
-                    umma_tmem_a(tmem + kPfColO + x * kPfTile, tmem + kPfColS + x * kPfTile + ks * 8,
-                                dv + (uint64_t)(ks * 256), id_pv, acc || ks > 0);
-                umma_commit(b_pv0 + 8 * x);
+                    for (int ks = 0; ks < kPfTile / 16; ++ks)
+                        umma_tmem_a(tmem + kPfColO + x * kPfTile, tmem + kPfColS + x * kPfTile + ks * 8,
+                                    dv + (uint64_t)(ks * 256), id_pv, acc || ks > 0);
+                    umma_commit(b_pv0 + 8 * x);
+                }
+                __syncwarp();
             };
             auto wait_full = [&](int T) {
-                if (!mbar_wait_bounded(full(T % kPfStages), (T / kPfStages) & 1, abort_flag, a.err_flag)) return false;
+                if (!__all_sync(kPfFull, mbar_wait_bounded(full(T % kPfStages), (T / kPfStages) & 1, abort_flag, a.err_flag)))
+                    return false;
                 tc_fence_after();
                 return true;
             };
@@ -435,8 +445,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attn_kernel(const Prefi
                 const int ntiles = max(nt_a, nt_b);
                 // both query tiles of the item in shared memory; their groups may then write the next item's
                 for (int x = 0; x < 2 && ok; ++x) {
-                    ok = mbar_wait_bounded(b_q0 + 8 * x, ni & 1, abort_flag, a.err_flag);
-                    mbar_arrive(b_qf0 + 8 * x);
+                    ok = __all_sync(kPfFull, mbar_wait_bounded(b_q0 + 8 * x, ni & 1, abort_flag, a.err_flag));
+                    if (one) mbar_arrive(b_qf0 + 8 * x);
                 }
                 tc_fence_after();
                 if (!ok || !wait_full(T0)) {
@@ -447,7 +457,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attn_kernel(const Prefi
                 if (nt_b > 0) qk(1, T0);
                 for (int t = 0; ok && t < ntiles; ++t) {
                     if (t < nt_a) {
-                        if (!mbar_wait_bounded(b_p0, np[0]++ & 1, abort_flag, a.err_flag)) {
+                        if (!__all_sync(kPfFull, mbar_wait_bounded(b_p0, np[0]++ & 1, abort_flag, a.err_flag))) {
                             ok = false;
                             break;
                         }
@@ -461,20 +471,20 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attn_kernel(const Prefi
                     }
                     if (t + 1 < nt_a) qk(0, T0 + t + 1);
                     if (t < nt_b) {
-                        if (!mbar_wait_bounded(b_p0 + 8, np[1]++ & 1, abort_flag, a.err_flag)) {
+                        if (!__all_sync(kPfFull, mbar_wait_bounded(b_p0 + 8, np[1]++ & 1, abort_flag, a.err_flag))) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
                         pv(1, T0 + t, t > 0);
                     }
-                    umma_commit(empty((T0 + t) % kPfStages));   // the stage's K and V are read once these complete
+                    if (one) umma_commit(empty((T0 + t) % kPfStages));   // the stage's K and V are read once these complete
                     if (t + 1 < nt_b) qk(1, T0 + t + 1);
                 }
                 T0 += ntiles;
             }
             // every MMA issued so far completes before the tensor memory is freed
-            umma_commit(b_drain);
+            if (one) umma_commit(b_drain);
             mbar_wait_bounded(b_drain, 0, nullptr, a.err_flag, 100000000ull);
         }
         __syncwarp();
