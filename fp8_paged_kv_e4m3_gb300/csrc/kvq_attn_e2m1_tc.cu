@@ -14,10 +14,15 @@
 //    K = code * block scale (exact fp16) to tensor memory -- the A operand of
 //    S^T = K Q^T -- and V to shared memory, MN-major -- the A operand of
 //    O^T = V^T P^T.  K and V are double-buffered.
-//  * warp 8: one thread issues the MMAs, S^T of tile t + 1 before P V of tile t.
-//  * warps 0-3 (softmax): thread = token; a row's reference moves only when a
-//    score rises more than 2^8 above it, decided by one OR-reduction of the four
-//    warps a tile; P^T (fp16) to shared memory; row sums in registers.
+//  * warp 12 issues the MMAs, S^T of tile t + 1 before P V of tile t.
+//  * warps 0-3 and 8-11 (softmax): thread = token and half of the rows (with all
+//    32 rows in one thread the softmax was a tile's longest chain: 153 -> 143 us);
+//    a row's reference moves only when a score rises more than 2^8 above it,
+//    decided by one OR-reduction of a half's four warps a tile; P^T (fp16) to
+//    shared memory; row sums in registers.
+// 64 sequences of 1K to 32K, 32 rows, 4 splits: 143 us, 2.3 TB/s of pages (one CTA
+// takes about 1.5 us a tile, two on an SM 1.06 us a tile together); the mma.sync
+// kernel takes 210 us.
 // Every wait is bounded (about 2 s): on expiry the CTA reports
 // KVQ_DEV_TIMEOUT, lets its copies and MMAs drain, gives its rows zero weight
 // and frees its tensor memory.
@@ -37,8 +42,8 @@ namespace {
 constexpr int kVtD = 128;
 constexpr int kVtTile = 128;                       // tokens per tile
 constexpr int kVtPages = kVtTile / 4;
-constexpr int kVtDecode = 4, kVtMma = 8;           // first decode warp, the MMA warp
-constexpr int kVtThreads = 32 * 9;
+constexpr int kVtDecode = 4, kVtMma = 12;          // first decode warp, the MMA warp; the others do the softmax
+constexpr int kVtThreads = 32 * 13;
 constexpr int kVtPage = e2m1_page_bytes(kVtD);     // 288
 constexpr int kVtRaw = 8 * kVtPage;                // a decode warp's raw K (or V) of one tile
 constexpr float kNoRef = -1e30f;                   // reference of a row that has seen no token
@@ -47,14 +52,14 @@ template <int NR>
 struct VtLayout {
     static constexpr int kV = 0;                                  // [2] V^T: 128 ch x 128 tok fp16, MN-major
     static constexpr int kQ = kV + 2 * kVtTile * kVtD * 2;        // Q: NR x 128 fp16, K-major
-    static constexpr int kP = kQ + NR * 256;                      // P^T: NR x 128 tok fp16, MN-major
-    static constexpr int kRaw = kP + NR * 256;                    // [4 warps][K, V] raw pages
+    static constexpr int kP = kQ + NR * 256;                      // [2] P^T: NR x 128 tok fp16, MN-major
+    static constexpr int kRaw = kP + 2 * NR * 256;                // [4 warps][K, V] raw pages
     static constexpr int kNref = kRaw + 4 * 2 * kVtRaw;           // [4 warps][NR] float: minus the reference
     static constexpr int kCorr = kNref + 4 * NR * 4;              // [4 warps][NR] float
     static constexpr int kWmax = kCorr + 4 * NR * 4;              // [4 warps][NR] float: maxima, then sums
     static constexpr int kBar = kWmax + 4 * NR * 4;
-    // barriers: k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full, drain
-    static constexpr int kNumBars = 12;
+    // barriers: k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], drain
+    static constexpr int kNumBars = 13;
     static constexpr int kAbort = kBar + 8 * kNumBars;
     static constexpr int kTmemSlot = kAbort + 8;
     static constexpr int kBytes = kTmemSlot + 8;
@@ -85,14 +90,24 @@ __device__ __forceinline__ void wait_copies()
     asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
 
-// OR of `x` over the `count` threads of named barrier `id`
-__device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t count, bool x)
+// Named barriers 1 and 2 of 128 threads, one for each half of the softmax warps (with the number an
+// immediate: a barrier number in a register reserves all sixteen).  The first also ORs `x`.
+template <int ID>
+__device__ __forceinline__ bool bar_or_id(bool x)
 {
     uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
-                 "barrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(r) : "r"(id), "r"(count), "r"(x ? 1u : 0u) : "memory");
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+                 "barrier.cta.red.or.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r) : "n"(ID), "r"(x ? 1u : 0u) : "memory");
     return r != 0;
+}
+
+__device__ __forceinline__ bool half_or(int half, bool x) { return half ? bar_or_id<2>(x) : bar_or_id<1>(x); }
+
+__device__ __forceinline__ void half_sync(int half)
+{
+    if (half) asm volatile("bar.sync 2, 128;" ::: "memory");
+    else asm volatile("bar.sync 1, 128;" ::: "memory");
 }
 
 // one row's 128 codes (16 words) times their block scales, as fp16 pairs of adjacent
@@ -141,7 +156,8 @@ template <int NR>
 __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_kernel(const AttnArgs a)
 {
     using T = VtLayout<NR>;
-    constexpr int D = kVtD, NH = (NR + 31) / 32;
+    static_assert(NR == 32 || NR == 64, "a half has 16 or 32 rows");
+    constexpr int D = kVtD;
     extern __shared__ __align__(128) uint8_t smem[];
     const int s = blockIdx.x, g = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -151,7 +167,8 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
     auto v_full = [&](int x) { return bar + 32 + 8 * x; };
     auto v_empty = [&](int x) { return bar + 48 + 8 * x; };
     auto s_full = [&](int x) { return bar + 64 + 8 * x; };
-    const uint32_t p_full = bar + 80, b_drain = bar + 88;
+    auto p_full = [&](int x) { return bar + 80 + 8 * x; };
+    const uint32_t b_drain = bar + 96;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + T::kAbort);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + T::kTmemSlot);
 
@@ -162,8 +179,8 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
             mbar_init(v_full(x), 4);
             mbar_init(v_empty(x), 1);
             mbar_init(s_full(x), 1);
+            mbar_init(p_full(x), 8);
         }
-        mbar_init(p_full, 4);
         mbar_init(b_drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -231,14 +248,14 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
                 const int x = t & 1;
                 if (t + 1 < ntiles && !scores(t + 1)) break;
                 if (!__all_sync(kFull, wait_for(v_full(x), (t >> 1) & 1, abort_flag, a.err_flag))) break;
-                if (!__all_sync(kFull, wait_for(p_full, t & 1, abort_flag, a.err_flag))) break;
+                if (!__all_sync(kFull, wait_for(p_full(x), (t >> 1) & 1, abort_flag, a.err_flag))) break;
                 tc_fence_after();
                 // O^T[ch][row] += sum_tok V[tok][ch] P[tok][row], both MN-major
-                const uint64_t dv = dv0 + (uint64_t)(x * (kVtTile * D * 2 / 16));
+                const uint64_t dv = dv0 + (uint64_t)(x * (kVtTile * D * 2 / 16)), dpx = dp + (uint64_t)(x * NR * 16);
                 if (one) {
 #pragma unroll
                     for (int ks = 0; ks < kVtTile / 16; ++ks)
-                        umma_smem_a(tmem + T::kColO, dv + (uint64_t)(ks * 2 * (D / 8) * 8), dp + (uint64_t)(ks * 2 * NR), id_pv,
+                        umma_smem_a(tmem + T::kColO, dv + (uint64_t)(ks * 2 * (D / 8) * 8), dpx + (uint64_t)(ks * 2 * NR), id_pv,
                                     t > 0 || ks > 0);
                     umma_commit(v_empty(x));
                 }
@@ -249,7 +266,7 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
             mbar_wait_bounded(b_drain, 0, nullptr, a.err_flag, 100000000ull);
         }
         __syncwarp();
-    } else if (warp >= kVtDecode) {
+    } else if (warp >= kVtDecode && warp < kVtDecode + 4) {
         // ================= decode warps =================
         const int d = warp - kVtDecode;
         const uint32_t lane_base = (uint32_t)(32 * d) << 16;
@@ -357,23 +374,22 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
         (void)ok;
         wait_copies<0>();
     } else {
-        // ================= softmax warps: thread = token =================
-        const int q = warp;
+        // ================= softmax warps: thread = token and half of the rows =================
+        constexpr int NH2 = NR / 2;                  // rows of a half
+        const int q = warp & 3, half = warp >> 3, r0 = half * NH2;
         const uint32_t lane_base = (uint32_t)(32 * q) << 16;
         const int tt = 32 * q + lane;
         const int win0 = L - a.q_len;                // row i of the window sees positions <= win0 + i
-        float *nref = reinterpret_cast<float *>(smem + T::kNref) + q * NR;
-        float *corr = reinterpret_cast<float *>(smem + T::kCorr) + q * NR;
-        float *wmax = reinterpret_cast<float *>(smem + T::kWmax);
+        float *nref = reinterpret_cast<float *>(smem + T::kNref) + q * NR + r0;   // from this half's first row on
+        float *corr = reinterpret_cast<float *>(smem + T::kCorr) + q * NR + r0;
+        float *wmax = reinterpret_cast<float *>(smem + T::kWmax) + r0;
         const float qk = a.qk_scale_log2;
         const float2 qk2 = make_float2(qk, qk);
-#pragma unroll
-        for (int h = 0; h < NH; ++h)
-            if (32 * h + lane < NR) nref[32 * h + lane] = -kNoRef;
+        if (lane < NH2) nref[lane] = -kNoRef;
         __syncwarp();
-        float2 l2[NR / 2];                           // this thread's sums of P, by row
+        float2 l2[NH2 / 2];                           // this thread's sums of P, by row
 #pragma unroll
-        for (int r = 0; r < NR / 2; ++r) l2[r] = make_float2(0.f, 0.f);
+        for (int r = 0; r < NH2 / 2; ++r) l2[r] = make_float2(0.f, 0.f);
         // the page of this thread's token (-1: past the split's end); the decode warps report bad ones
         const unsigned num_pages = (unsigned)min(a.num_pages, (int64_t)0x80000000ll);
         auto token_page = [&](int t) {
@@ -382,55 +398,63 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
         };
         int page = token_page(0);
         bool ok = true;
+#ifdef KVQ_TEST_STALL_SOFTMAX
+        // Test builds only (never the library's default build): a wait, bounded by KVQ_TEST_STALL_SOFTMAX
+        // nanoseconds, for the first P V, which needs the P of these warps: it always gives up.
+        ok = __all_sync(kFull, mbar_wait_bounded(v_empty(0), 0, abort_flag, a.err_flag, KVQ_TEST_STALL_SOFTMAX));
+#endif
         for (int t = 0; t < ntiles; ++t) {
             const int x = t & 1;
             const unsigned have = __ballot_sync(kFull, (unsigned)page < num_pages);   // tokens with a page
             page = token_page(t + 1);
             ok = ok && __all_sync(kFull, wait_for(s_full(x), (t >> 1) & 1, abort_flag, a.err_flag));
             tc_fence_after();
-            float2 z[NR / 2];
+            float2 z[NH2 / 2];
+            {
+                uint32_t r16[NH2 / 16][16];
 #pragma unroll
-            for (int c = 0; c < NR; c += 16) {
-                uint32_t r16[16];
-                tmem_ld16(tmem + lane_base + T::kColS + x * NR + c, r16);
+                for (int c = 0; c < NH2 / 16; ++c) tmem_ld16(tmem + lane_base + T::kColS + x * NR + r0 + 16 * c, r16[c]);
                 tmem_wait_ld();
-                tmem_regs_ready(r16);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    z[c / 2 + e] = make_float2(__uint_as_float(r16[2 * e]), __uint_as_float(r16[2 * e + 1]));
+                for (int c = 0; c < NH2 / 16; ++c) {
+                    tmem_regs_ready(r16[c]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        z[8 * c + e] = make_float2(__uint_as_float(r16[c][2 * e]), __uint_as_float(r16[c][2 * e + 1]));
+                }
             }
             // rows of window row i see positions <= win0 + i; tokens without a page none
             const int pos = (item0 + t * kVtPages) * 4 + tt;
             if (have != kFull || (item0 + (t + 1) * kVtPages) > (win0 + 1) / 4) {
                 const int first = !((have >> lane) & 1u) ? NR : pos > win0 ? a.group * (pos - win0) : 0;
 #pragma unroll
-                for (int r = 0; r < NR / 2; ++r) {
-                    if (2 * r < first) z[r].x = -INFINITY;
-                    if (2 * r + 1 < first) z[r].y = -INFINITY;
+                for (int r = 0; r < NH2 / 2; ++r) {
+                    if (r0 + 2 * r < first) z[r].x = -INFINITY;
+                    if (r0 + 2 * r + 1 < first) z[r].y = -INFINITY;
                 }
             }
             // z = score - reference (log2 units)
             float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int r = 0; r < NR / 2; r += 2) {
+            for (int r = 0; r < NH2 / 2; r += 2) {
                 const float4 nr = *reinterpret_cast<const float4 *>(nref + 2 * r);
                 z[r] = ffma2(z[r], qk2, make_float2(nr.x, nr.y));
                 z[r + 1] = ffma2(z[r + 1], qk2, make_float2(nr.z, nr.w));
                 m4[(r / 2) & 3] = fmax3(fmax3(m4[(r / 2) & 3], z[r].x, z[r].y), z[r + 1].x, z[r + 1].y);
             }
             const bool above = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) > 8.f;
-            if (named_bar_or(1, 128, above || !ok)) {
+            if (half_or(half, above || !ok)) {
                 // rare: exact maxima of the tile's rows, references that rose by more than 2^8, O and the sums rescaled
-                if (named_bar_or(1, 128, !ok)) {     // some warp gave up: all four leave together
+                if (half_or(half, !ok)) {     // some warp gave up: all four leave together
                     ok = false;
                     break;
                 }
                 // the scores themselves again (z of a row without a reference has lost them)
                 auto reload = [&](bool absolute) {
 #pragma unroll
-                    for (int c = 0; c < NR; c += 16) {
+                    for (int c = 0; c < NH2; c += 16) {
                         uint32_t r16[16];
-                        tmem_ld16(tmem + lane_base + T::kColS + x * NR + c, r16);
+                        tmem_ld16(tmem + lane_base + T::kColS + x * NR + r0 + c, r16);
                         tmem_wait_ld();
                         tmem_regs_ready(r16);
 #pragma unroll
@@ -445,34 +469,28 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
                     }
                 };
                 reload(true);
-#pragma unroll
-                for (int h = 0; h < NH; ++h) {
+                {
                     float v[32];
 #pragma unroll
-                    for (int r = 0; r < 32; ++r) {
-                        const int i = (32 * h + r) / 2 % (NR / 2);
-                        v[r] = 32 * h + r < NR ? ((r & 1) ? z[i].y : z[i].x) : -INFINITY;
-                    }
+                    for (int r = 0; r < 32; ++r)
+                        v[r] = r < NH2 ? ((r & 1) ? z[r / 2 % (NH2 / 2)].y : z[r / 2 % (NH2 / 2)].x) : -INFINITY;
                     const float m = across_lanes<true>(v, lane);
-                    if (32 * h + lane < NR) wmax[q * NR + 32 * h + lane] = m;
+                    if (lane < NH2) wmax[q * NR + lane] = m;
                 }
-                named_bar_sync(1, 128);
-#pragma unroll
-                for (int h = 0; h < NH; ++h) {
-                    const int r = 32 * h + lane;
-                    if (r >= NR) continue;
+                half_sync(half);
+                if (lane < NH2) {
                     float m = -INFINITY;
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) m = fmaxf(m, wmax[w * NR + r]);
-                    const float old = -nref[r];
+                    for (int w = 0; w < 4; ++w) m = fmaxf(m, wmax[w * NR + lane]);
+                    const float old = -nref[lane];
                     const bool move = m > old + 8.f;
-                    corr[r] = move ? fast_exp2(old - m) : 1.f;   // 0 where there was no reference
-                    if (move) nref[r] = -m;
+                    corr[lane] = move ? fast_exp2(old - m) : 1.f;   // 0 where there was no reference
+                    if (move) nref[lane] = -m;
                 }
                 __syncwarp();
                 reload(false);
 #pragma unroll
-                for (int r = 0; r < NR / 2; ++r) {
+                for (int r = 0; r < NH2 / 2; ++r) {
                     l2[r].x *= corr[2 * r];
                     l2[r].y *= corr[2 * r + 1];
                 }
@@ -480,25 +498,25 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
                 tc_fence_after();
                 if (t > 0) {
 #pragma unroll
-                    for (int c = 0; c < NR; c += 16) {
+                    for (int c = 0; c < NH2; c += 16) {
                         uint32_t r16[16];
-                        tmem_ld16(tmem + lane_base + T::kColO + c, r16);
+                        tmem_ld16(tmem + lane_base + T::kColO + r0 + c, r16);
                         tmem_wait_ld();
                         tmem_regs_ready(r16);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) r16[e] = __float_as_uint(__uint_as_float(r16[e]) * corr[c + e]);
-                        tmem_st16(tmem + lane_base + T::kColO + c, r16);
+                        tmem_st16(tmem + lane_base + T::kColO + r0 + c, r16);
                     }
                     tmem_wait_st();
                 }
-                named_bar_sync(1, 128);              // the maxima have been read
+                half_sync(half);              // the maxima have been read
             }
-            // P = 2^z; P^T: (row, tok) at (tok/8) * NR*16 + (row/8) * 128 + (tok%8) * 16.  The previous tile's
-            // P V has read it.
-            if (t > 0) ok = ok && __all_sync(kFull, wait_for(v_empty((t - 1) & 1), ((t - 1) >> 1) & 1, abort_flag, a.err_flag));
-            uint8_t *dst = smem + T::kP + (tt >> 3) * (NR * 16) + (tt & 7) * 16;
+            // P = 2^z; P^T: (row, tok) at (tok/8) * NR*16 + (row/8) * 128 + (tok%8) * 16, once the P V of two tiles
+            // ago has read the buffer
+            if (t > 1) ok = ok && __all_sync(kFull, wait_for(v_empty(x), ((t >> 1) - 1) & 1, abort_flag, a.err_flag));
+            uint8_t *dst = smem + T::kP + x * NR * 256 + (tt >> 3) * (NR * 16) + (tt & 7) * 16;
 #pragma unroll
-            for (int c = 0; c < NR / 8; ++c) {
+            for (int c = 0; c < NH2 / 8; ++c) {
                 uint32_t w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -506,60 +524,53 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
                     l2[4 * c + e] = fadd2(l2[4 * c + e], p);
                     w[e] = pack_half2(p.x, p.y);
                 }
-                *reinterpret_cast<uint4 *>(dst + c * 128) = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4 *>(dst + (r0 / 8 + c) * 128) = make_uint4(w[0], w[1], w[2], w[3]);
             }
             fence_async_smem();
             tc_fence_before();
             __syncwarp();
-            if (ok && lane == 0) mbar_arrive(p_full);
+            if (ok && lane == 0) mbar_arrive(p_full(x));
         }
         // ---- epilogue: row sums over the four warps, then O^T / l ----
-#pragma unroll
-        for (int h = 0; h < NH; ++h) {
+        {
             float v[32];
 #pragma unroll
-            for (int r = 0; r < 32; ++r)
-                v[r] = 32 * h + r < NR ? ((r & 1) ? l2[(32 * h + r) / 2 % (NR / 2)].y : l2[(32 * h + r) / 2 % (NR / 2)].x) : 0.f;
+            for (int r = 0; r < 32; ++r) v[r] = r < NH2 ? ((r & 1) ? l2[r / 2 % (NH2 / 2)].y : l2[r / 2 % (NH2 / 2)].x) : 0.f;
             const float l = across_lanes<false>(v, lane);
-            if (32 * h + lane < NR) wmax[q * NR + 32 * h + lane] = l;
+            if (lane < NH2) wmax[q * NR + lane] = l;
         }
         if (ok && ntiles > 0)
             ok = __all_sync(kFull, wait_for(v_empty((ntiles - 1) & 1), ((ntiles - 1) >> 1) & 1, abort_flag, a.err_flag));
-        if (!named_bar_or(1, 128, !ok)) {
+        if (!half_or(half, !ok)) {
             tc_fence_after();
             const int S = a.num_splits;
-            int unit_l[NH];                          // row's workspace unit (lane r, and r + 32), -1 for a padding row
-            float coef_l[NH];
-#pragma unroll
-            for (int h = 0; h < NH; ++h) {
-                const int r = 32 * h + lane;
-                unit_l[h] = -1;
-                coef_l[h] = 0.f;
-                if (r >= a.rows || r >= NR) continue;
+            int unit_l = -1;                         // lane r: the workspace unit of this half's row r, -1 for a padding row
+            float coef_l = 0.f;
+            if (lane < NH2 && r0 + lane < a.rows) {
+                const int r = r0 + lane;
                 float l = 0.f;
 #pragma unroll
-                for (int w = 0; w < 4; ++w) l += wmax[w * NR + r];
+                for (int w = 0; w < 4; ++w) l += wmax[w * NR + lane];
                 const int i = r / a.group, hh = g * a.group + r % a.group;
-                unit_l[h] = ((b * a.num_q_heads + hh) * a.q_len + i) * S + s;
+                unit_l = ((b * a.num_q_heads + hh) * a.q_len + i) * S + s;
                 const bool nan = l != l;             // a NaN score: the split outweighs every other in the combine
-                coef_l[h] = l == 0.f ? 0.f : a.out_scale / l;
+                coef_l = l == 0.f ? 0.f : a.out_scale / l;
                 if (q == 0) {
-                    a.ws_m[unit_l[h]] = nan ? FLT_MAX : l > 0.f ? -nref[r] * kLn2 : -INFINITY;
-                    a.ws_l[unit_l[h]] = nan ? 1.f : l;
+                    a.ws_m[unit_l] = nan ? FLT_MAX : l > 0.f ? -nref[lane] * kLn2 : -INFINITY;
+                    a.ws_l[unit_l] = nan ? 1.f : l;
                 }
             }
             if (ntiles > 0) {
 #pragma unroll
-                for (int c = 0; c < NR; c += 16) {
+                for (int c = 0; c < NH2; c += 16) {
                     uint32_t r16[16];
-                    tmem_ld16(tmem + lane_base + T::kColO + c, r16);
+                    tmem_ld16(tmem + lane_base + T::kColO + r0 + c, r16);
                     tmem_wait_ld();
                     tmem_regs_ready(r16);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const int r = c + e;
-                        const int unit = __shfl_sync(kFull, unit_l[r / 32], r % 32);
-                        const float k = __shfl_sync(kFull, coef_l[r / 32], r % 32);
+                        const int unit = __shfl_sync(kFull, unit_l, c + e);
+                        const float k = __shfl_sync(kFull, coef_l, c + e);
                         if (unit >= 0 && k != 0.f) a.ws_o[(int64_t)unit * D + tt] = __uint_as_float(r16[e]) * k;
                     }
                 }
@@ -570,8 +581,8 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
     // ---- teardown: copies landed (each decode warp waited), MMAs complete, tensor memory freed ----
     tc_fence_before();
     __syncthreads();
-    if (*abort_flag && warp < 4) {
-        for (int r = threadIdx.x; r < a.rows; r += 128) {
+    if (*abort_flag) {
+        for (int r = threadIdx.x; r < a.rows; r += kVtThreads) {
             const int i = r / a.group, hh = g * a.group + r % a.group;
             const int64_t unit = (((int64_t)b * a.num_q_heads + hh) * a.q_len + i) * a.num_splits + s;
             a.ws_m[unit] = -INFINITY;

@@ -463,6 +463,31 @@ def test_decode_pages_beyond_4_gib():
     assert np.array_equal(k.cpu().numpy(), (E.values(*E.quantize(rows[0][-3:], ks)).astype(np.float32) * np.float32(ks)).astype(np.float16))
 
 
+@pytest.mark.parametrize("Hq,splits", [(8, 1), (8, 3), (16, 2)])
+def test_tensor_core_kernel_gives_up_cleanly(Hq, splits):
+    """A wait that runs out (a test build whose softmax warps first wait, 20 us long, for a product of their own): the
+    error bit, empty partials, nothing hung, and the context usable."""
+    import ctypes
+    lib = kvq.load(build.build_variant("stall_softmax", {"KVQ_TEST_STALL_SOFTMAX": "20000ull"}, ("kvq_attn_e2m1_tc.cu",)))
+    pr = _problem(24, 2, 4, Hq, 1, 128, [3000, 517])
+    q, kc, vc, bt, lens = (to_dev(a) for a in pr[:5])
+    p = kvq.attn_params(q, 1, bt.shape[1], splits)
+    ws = kvq.alloc_workspace(p, "cuda").fill_(float("nan"))
+    err = _err()
+    ptr = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    st = lib.paged_decode_attn_e2m1_partial(ptr(q), ptr(kc), ptr(vc), kc.shape[0], ptr(bt), ptr(lens), ctypes.c_float(pr[5]),
+                                            ctypes.c_float(pr[6]), None, None, ptr(ws), ws.numel() * 4, ctypes.byref(p), ptr(err),
+                                            ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    assert st == 0 and err.item() == kvq.DEV_TIMEOUT
+    _, m, l = kvq.workspace_views(ws, p)
+    assert torch.isneginf(m).all() and (l == 0).all()
+    out, err = _run(*pr, num_splits=splits)                # the library's own build, right after
+    ref, tol, flags = E.decode(*pr)
+    assert err == flags == 0
+    E.close(out, ref, tol)
+
+
 # --- prefill ---------------------------------------------------------------
 
 @pytest.mark.parametrize("chunks,history,Hq,Hkv", [([1], [0], 4, 1), ([37, 1, 200], [5, 300, 0], 8, 2), ([129, 256], [127, 1], 4, 4)])
