@@ -296,28 +296,34 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
             const int it = item0 + t * kVtPages + 8 * d + (lane & 7);
             return it < item1 ? __ldg(sr.bt_row + it) : -1;
         };
+        const unsigned num_pages = (unsigned)min(a.num_pages, (int64_t)0x80000000ll);
         auto checked = [&](int phys, int t) {
-            if (phys >= 0 && (int64_t)phys < a.num_pages) return phys;
+            if (__builtin_expect((unsigned)phys < num_pages, 1)) return phys;
             if (item0 + t * kVtPages + 8 * d + (lane & 7) < item1 && lane < 8) report(a.err_flag, KVQ_DEV_BAD_PAGE);
             return -1;
         };
         // 8 pages as 144 pieces of 16 bytes, consecutive lanes on consecutive pieces; missing
         // pages are read from page 0 (whatever it holds) and masked
-        auto fetch = [&](const uint8_t *pool, uint32_t dst, int phys) {
+        int piece[5];                       // the page of this lane's i-th piece
+        auto pieces = [&](int phys) {
             const int have = max(phys, 0);
+#pragma unroll
+            for (int i = 0; i < 5; ++i) piece[i] = __shfl_sync(kFull, have, (((i * 32 + lane) * 57) >> 10) & 7);
+        };
+        auto fetch = [&](const uint8_t *pool, uint32_t dst) {
 #pragma unroll
             for (int i = 0; i < 5; ++i) {
                 const int c = i * 32 + lane, p = (c * 57) >> 10;   // c / 18 for c < 144
-                const int page = __shfl_sync(kFull, have, p & 7);
-                if (c < 8 * (kVtPage / 16)) copy16(dst + c * 16, pool + page * page_stride + (c * 16 - p * kVtPage));
+                if (c < 8 * (kVtPage / 16)) copy16(dst + c * 16, pool + piece[i] * page_stride + (c * 16 - p * kVtPage));
             }
             commit_copies();
         };
         int cur = -1, nxt = raw_page(1);
         if (ntiles > 0) {
             cur = checked(raw_page(0), 0);
-            fetch(kpool, rawk_s, cur);
-            fetch(vpool, rawv_s, cur);
+            pieces(cur);
+            fetch(kpool, rawk_s);
+            fetch(vpool, rawv_s);
         }
         const int row_off = (lane >> 2) * kVtPage + (lane & 3) * (D / 2), scale_off = (lane >> 2) * kVtPage + 2 * D;
         const uint32_t sel = 0x11u * (lane & 3);            // this token's byte of a scale word, twice
@@ -328,6 +334,7 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
             const bool more = t + 1 < ntiles;
             const int ahead = raw_page(t + 2);
             if (more) nxt = checked(nxt, t + 1);
+            pieces(nxt);
             // this warp's tokens of the tile: inside a page that exists, below L
             const int pos = (item0 + t * kVtPages + 8 * d) * 4 + lane;
             const bool live = __shfl_sync(kFull, cur, lane >> 2) >= 0 && pos < L;
@@ -340,7 +347,7 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
 #pragma unroll
             for (int u = 0; u < 2; ++u) sc[u] = *reinterpret_cast<const uint4 *>(rawk + scale_off + 16 * u);
             __syncwarp();
-            if (more) fetch(kpool, rawk_s, nxt);
+            if (more) fetch(kpool, rawk_s);
             else commit_copies();
             if (t >= 2 && !wait_for(k_empty(x), ((t >> 1) - 1) & 1, abort_flag, a.err_flag)) {
                 ok = false;
@@ -368,7 +375,7 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
 #pragma unroll
             for (int u = 0; u < 2; ++u) sc[u] = *reinterpret_cast<const uint4 *>(rawv + scale_off + 16 * u);
             __syncwarp();
-            if (more) fetch(vpool, rawv_s, nxt);
+            if (more) fetch(vpool, rawv_s);
             else commit_copies();
             if (t >= 2 && !wait_for(v_empty(x), ((t >> 1) - 1) & 1, abort_flag, a.err_flag)) {
                 ok = false;
@@ -459,7 +466,7 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
                 m4[(r / 2) & 3] = fmax3(fmax3(m4[(r / 2) & 3], z[r].x, z[r].y), z[r + 1].x, z[r + 1].y);
             }
             const bool above = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) > 8.f;
-            if (half_or(half, above || !ok)) {
+            if (__builtin_expect(half_or(half, above || !ok), 0)) {
                 // rare: exact maxima of the tile's rows, references that rose by more than 2^8, O and the sums rescaled
                 if (half_or(half, !ok)) {     // some warp gave up: all four leave together
                     ok = false;
