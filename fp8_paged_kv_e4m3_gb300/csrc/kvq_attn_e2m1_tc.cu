@@ -71,28 +71,6 @@ struct VtLayout {
     static constexpr int kCols = 128 + 3 * NR <= 256 ? 256 : 512;
 };
 
-// A whole warp's bounded wait.  Every try is followed by a vote, so that the branch is the warp's: with
-// each lane leaving the loop by itself a wait for a phase long complete took 200 to 400 cycles.
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int *abort, int32_t *err_flag)
-{
-    if (__builtin_expect(__all_sync(kFull, mbar_try_wait(bar, parity)), 1)) return true;
-    uint64_t t0 = 0;
-#pragma unroll 1
-    for (uint32_t it = 1;; ++it) {
-        if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
-        if ((it & 63u) == 0u) {
-            if (__any_sync(kFull, *abort != 0)) return false;
-            const uint64_t now = global_timer_ns();
-            if (t0 == 0) t0 = now;
-            if (__any_sync(kFull, now - t0 > kWaitLimitNs)) {
-                *abort = 1;
-                report(err_flag, KVQ_DEV_TIMEOUT);
-                return false;
-            }
-        }
-    }
-}
-
 __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -246,7 +224,7 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
             // S^T[tok][row] = sum_d K[tok][d] Q[row][d]
             auto scores = [&](int t) {
                 const int x = t & 1;
-                if (!wait_for(k_full(x), (t >> 1) & 1, abort_flag, a.err_flag)) return false;
+                if (!mbar_wait_warp(k_full(x), (t >> 1) & 1, abort_flag, a.err_flag)) return false;
                 tc_fence_after();
                 if (one) {
 #pragma unroll
@@ -263,8 +241,8 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
             for (int t = 0; ok && t < ntiles; ++t) {
                 const int x = t & 1;
                 if (t + 1 < ntiles && !scores(t + 1)) break;
-                if (!wait_for(v_full(x), (t >> 1) & 1, abort_flag, a.err_flag)) break;
-                if (!wait_for(p_full(x), (t >> 1) & 1, abort_flag, a.err_flag)) break;
+                if (!mbar_wait_warp(v_full(x), (t >> 1) & 1, abort_flag, a.err_flag)) break;
+                if (!mbar_wait_warp(p_full(x), (t >> 1) & 1, abort_flag, a.err_flag)) break;
                 tc_fence_after();
                 // O^T[ch][row] += sum_tok V[tok][ch] P[tok][row], both MN-major
                 const uint64_t dv = dv0 + (uint64_t)(x * (kVtTile * D * 2 / 16)), dpx = dp + (uint64_t)(x * NR * 16);
@@ -349,7 +327,7 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
             __syncwarp();
             if (more) fetch(kpool, rawk_s);
             else commit_copies();
-            if (t >= 2 && !wait_for(k_empty(x), ((t >> 1) - 1) & 1, abort_flag, a.err_flag)) {
+            if (t >= 2 && !mbar_wait_warp(k_empty(x), ((t >> 1) - 1) & 1, abort_flag, a.err_flag)) {
                 ok = false;
                 break;
             }
@@ -377,7 +355,7 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
             __syncwarp();
             if (more) fetch(vpool, rawv_s);
             else commit_copies();
-            if (t >= 2 && !wait_for(v_empty(x), ((t >> 1) - 1) & 1, abort_flag, a.err_flag)) {
+            if (t >= 2 && !mbar_wait_warp(v_empty(x), ((t >> 1) - 1) & 1, abort_flag, a.err_flag)) {
                 ok = false;
                 break;
             }
@@ -430,7 +408,7 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
             const int x = t & 1;
             const unsigned have = __ballot_sync(kFull, (unsigned)page < num_pages);   // tokens with a page
             page = token_page(t + 1);
-            ok = ok && wait_for(s_full(x), (t >> 1) & 1, abort_flag, a.err_flag);
+            ok = ok && mbar_wait_warp(s_full(x), (t >> 1) & 1, abort_flag, a.err_flag);
             tc_fence_after();
             float2 z[NH2 / 2];
             {
@@ -517,7 +495,7 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
                     l2[r].x *= corr[2 * r];
                     l2[r].y *= corr[2 * r + 1];
                 }
-                if (t > 0) ok = ok && wait_for(v_empty((t - 1) & 1), ((t - 1) >> 1) & 1, abort_flag, a.err_flag);
+                if (t > 0) ok = ok && mbar_wait_warp(v_empty((t - 1) & 1), ((t - 1) >> 1) & 1, abort_flag, a.err_flag);
                 tc_fence_after();
                 if (t > 0) {
 #pragma unroll
@@ -536,7 +514,7 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
             }
             // P = 2^z; P^T: (row, tok) at (tok/8) * NR*16 + (row/8) * 128 + (tok%8) * 16, once the P V of two tiles
             // ago has read the buffer
-            if (t > 1) ok = ok && wait_for(v_empty(x), ((t >> 1) - 1) & 1, abort_flag, a.err_flag);
+            if (t > 1) ok = ok && mbar_wait_warp(v_empty(x), ((t >> 1) - 1) & 1, abort_flag, a.err_flag);
             uint8_t *dst = smem + T::kP + x * NR * 256 + (tt >> 3) * (NR * 16) + (tt & 7) * 16;
 #pragma unroll
             for (int c = 0; c < NH2 / 8; ++c) {
@@ -563,7 +541,7 @@ __global__ void __launch_bounds__(kVtThreads, NR <= 32 ? 2 : 1) attn_e2m1_tc_ker
             if (lane < NH2) wmax[q * NR + lane] = l;
         }
         if (ok && ntiles > 0)
-            ok = wait_for(v_empty((ntiles - 1) & 1), ((ntiles - 1) >> 1) & 1, abort_flag, a.err_flag);
+            ok = mbar_wait_warp(v_empty((ntiles - 1) & 1), ((ntiles - 1) >> 1) & 1, abort_flag, a.err_flag);
         if (!half_or(half, !ok)) {
             tc_fence_after();
             const int S = a.num_splits;

@@ -28,7 +28,7 @@
 //     S = Q K^T runs during that epilogue.
 //       warp 8: one thread streams the K and V tiles (one 32 KB 1-D bulk copy
 //               each) through a 2-stage shared ring;
-//       warp 9: allocates tensor memory; one thread issues the MMAs:
+//       warp 9: allocates tensor memory; one elected lane issues the MMAs:
 //               S_X = Q_X K^T (M = 128 rows, N = 128 keys, K = 16 per
 //               instruction, both K-major in shared memory) and
 //               O_X += P_X V (P from tensor memory, V MN-major in shared
@@ -37,7 +37,7 @@
 //       warps 0-3 (tile A) and 4-7 (tile B): thread r of a group owns row r
 //               of its tile (tensor-memory lane r): reads its 128 scores,
 //               masks the causal diagonal, and writes P (fp16) over the S it
-//               read.  A row's reference moves only when a score rises more
+//               read, in two halves.  A row's reference moves only when a score rises more
 //               than 2^8 above it (the O row is then rescaled in tensor
 //               memory); the row sum stays in a register.
 //     Every wait is bounded (about 2 s); on expiry the CTA reports
@@ -63,6 +63,9 @@ constexpr int kPfTile = 128;                        // keys per KV tile = query 
 constexpr int kPfD = 128;                           // head_dim of this path
 constexpr int kPfTileBytes = kPfTile * kPfD * 2;    // one fp16 tile: 32 KB
 constexpr int kPfStages = 2;
+// P is handed over in halves, so that its product starts while the softmax writes the second (8192-token
+// chunk: 378 -> 355 us; in quarters 406)
+constexpr int kPfParts = 2;
 constexpr int kPfThreads = 320;
 constexpr int kPfSoftmaxWarps = 8;                  // two groups of 4, one per query tile
 constexpr int kPfLoadWarp = 8;
@@ -73,8 +76,8 @@ constexpr unsigned kPfFull = 0xFFFFFFFFu;
 constexpr int kPfQ = 0;
 constexpr int kPfRing = kPfQ + 2 * kPfTileBytes;
 constexpr int kPfBar = kPfRing + kPfStages * 2 * kPfTileBytes;
-// barriers: full[2], empty[2], q[2], q taken[2], s[2], p[2], pv[2], drain
-constexpr int kPfNumBars = 2 * kPfStages + 2 + 2 + 2 + 2 + 2 + 1;
+// barriers: full[2], empty[2], q[2], q taken[2], s[2], pv[2], drain, p[2][parts]
+constexpr int kPfNumBars = 2 * kPfStages + 2 + 2 + 2 + 2 + 1 + 2 * kPfParts;
 constexpr int kPfAbort = kPfBar + 8 * kPfNumBars;
 constexpr int kPfTmemSlot = kPfAbort + 8;
 constexpr int kPfCount = kPfTmemSlot + 8;           // the sorted pairs: count, then the entries
@@ -333,9 +336,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attn_kernel(const Prefi
     auto full = [&](int s) { return bar + 8 * s; };
     auto empty = [&](int s) { return bar + 8 * (kPfStages + s); };
     // per query tile X (at + 8 X): its Q written (softmax group -> MMA), its Q
-    // taken (MMA -> softmax group), S ready, P ready, P V complete
+    // taken (MMA -> softmax group), S ready, P V complete; P ready by parts
     const uint32_t b_q0 = bar + 8 * (2 * kPfStages);
-    const uint32_t b_qf0 = b_q0 + 16, b_s0 = b_q0 + 32, b_p0 = b_q0 + 48, b_pv0 = b_q0 + 64, b_drain = b_q0 + 80;
+    const uint32_t b_qf0 = b_q0 + 16, b_s0 = b_q0 + 32, b_pv0 = b_q0 + 48, b_drain = b_q0 + 64, b_p0 = b_q0 + 72;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kPfAbort);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kPfTmemSlot);
 
@@ -348,7 +351,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attn_kernel(const Prefi
             mbar_init(b_q0 + 8 * x, kPfSoftmaxWarps / 2);
             mbar_init(b_qf0 + 8 * x, 1);
             mbar_init(b_s0 + 8 * x, 1);
-            mbar_init(b_p0 + 8 * x, kPfSoftmaxWarps / 2);
+            for (int p = 0; p < kPfParts; ++p) mbar_init(b_p0 + 8 * (x * kPfParts + p), kPfSoftmaxWarps / 2);
             mbar_init(b_pv0 + 8 * x, 1);
         }
         mbar_init(b_drain, 1);
@@ -418,21 +421,29 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attn_kernel(const Prefi
                 }
                 __syncwarp();
             };
-            // O_X (+)= P_X V_T: A = P (tensor memory, two fp16 per column), B = V (MN-major)
-            auto pv = [&](int x, int T, bool acc) {
+            // O_X (+)= P_X V_T: A = P (tensor memory, two fp16 per column), B = V (MN-major); each part of the
+            // keys as soon as its P is there
+            auto pv = [&](int x, int T, int phase, bool acc) {
                 const uint32_t v_addr = smem_u32(smem + kPfRing + (T % kPfStages) * 2 * kPfTileBytes + kPfTileBytes);
                 const uint64_t dv = umma_desc(v_addr, 2048, 128);
-                if (one) {
+                constexpr int kSteps = kPfTile / 16 / kPfParts;
 #pragma unroll
-                    for (int ks = 0; ks < kPfTile / 16; ++ks)
-                        umma_tmem_a(tmem + kPfColO + x * kPfTile, tmem + kPfColS + x * kPfTile + ks * 8,
-                                    dv + (uint64_t)(ks * 256), id_pv, acc || ks > 0);
-                    umma_commit(b_pv0 + 8 * x);
+                for (int p = 0; p < kPfParts; ++p) {
+                    if (!mbar_wait_warp(b_p0 + 8 * (x * kPfParts + p), phase & 1, abort_flag, a.err_flag)) return false;
+                    tc_fence_after();
+                    if (one) {
+#pragma unroll
+                        for (int ks = p * kSteps; ks < (p + 1) * kSteps; ++ks)
+                            umma_tmem_a(tmem + kPfColO + x * kPfTile, tmem + kPfColS + x * kPfTile + ks * 8,
+                                        dv + (uint64_t)(ks * 256), id_pv, acc || ks > 0);
+                        if (p + 1 == kPfParts) umma_commit(b_pv0 + 8 * x);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                return true;
             };
             auto wait_full = [&](int T) {
-                if (!__all_sync(kPfFull, mbar_wait_bounded(full(T % kPfStages), (T / kPfStages) & 1, abort_flag, a.err_flag)))
+                if (!mbar_wait_warp(full(T % kPfStages), (T / kPfStages) & 1, abort_flag, a.err_flag))
                     return false;
                 tc_fence_after();
                 return true;
@@ -445,7 +456,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attn_kernel(const Prefi
                 const int ntiles = max(nt_a, nt_b);
                 // both query tiles of the item in shared memory; their groups may then write the next item's
                 for (int x = 0; x < 2 && ok; ++x) {
-                    ok = __all_sync(kPfFull, mbar_wait_bounded(b_q0 + 8 * x, ni & 1, abort_flag, a.err_flag));
+                    ok = mbar_wait_warp(b_q0 + 8 * x, ni & 1, abort_flag, a.err_flag);
                     if (one) mbar_arrive(b_qf0 + 8 * x);
                 }
                 tc_fence_after();
@@ -457,12 +468,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attn_kernel(const Prefi
                 if (nt_b > 0) qk(1, T0);
                 for (int t = 0; ok && t < ntiles; ++t) {
                     if (t < nt_a) {
-                        if (!__all_sync(kPfFull, mbar_wait_bounded(b_p0, np[0]++ & 1, abort_flag, a.err_flag))) {
+                        if (!pv(0, T0 + t, np[0]++, t > 0)) {
                             ok = false;
                             break;
                         }
-                        tc_fence_after();
-                        pv(0, T0 + t, t > 0);
                     }
                     const bool next = t + 1 < ntiles;
                     if (next && !wait_full(T0 + t + 1)) {
@@ -471,12 +480,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attn_kernel(const Prefi
                     }
                     if (t + 1 < nt_a) qk(0, T0 + t + 1);
                     if (t < nt_b) {
-                        if (!__all_sync(kPfFull, mbar_wait_bounded(b_p0 + 8, np[1]++ & 1, abort_flag, a.err_flag))) {
+                        if (!pv(1, T0 + t, np[1]++, t > 0)) {
                             ok = false;
                             break;
                         }
-                        tc_fence_after();
-                        pv(1, T0 + t, t > 0);
                     }
                     if (one) umma_commit(empty((T0 + t) % kPfStages));   // the stage's K and V are read once these complete
                     if (t + 1 < nt_b) qk(1, T0 + t + 1);
@@ -493,7 +500,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attn_kernel(const Prefi
         const int x = warp >> 2;                                // query tile
         const int r = 32 * (warp & 3) + lane;
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t b_q = b_q0 + 8 * x, b_qf = b_qf0 + 8 * x, b_s = b_s0 + 8 * x, b_p = b_p0 + 8 * x,
+        const uint32_t b_q = b_q0 + 8 * x, b_qf = b_qf0 + 8 * x, b_s = b_s0 + 8 * x, b_p = b_p0 + 8 * kPfParts * x,
                        b_pv = b_pv0 + 8 * x;
         const uint32_t sb = tmem + lane_base + kPfColS + x * kPfTile;
         const uint32_t ob = tmem + lane_base + kPfColO + x * kPfTile;
@@ -533,7 +540,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attn_kernel(const Prefi
             for (int t = 0; t < nt; ++t) {
                 // keys of this tile left out for a bad block-table entry (almost always none)
                 const uint4 badk = __ldg(reinterpret_cast<const uint4 *>(mask_row) + t);
-                if (!__all_sync(kPfFull, mbar_wait_bounded(b_s, (ns + t) & 1, abort_flag, a.err_flag))) {
+                if (!mbar_wait_warp(b_s, (ns + t) & 1, abort_flag, a.err_flag)) {
                     ok = false;
                     break;
                 }
@@ -584,7 +591,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attn_kernel(const Prefi
                     ref = mx;
                 }
                 if (t > 0 && __any_sync(kPfFull, move)) {
-                    if (!__all_sync(kPfFull, mbar_wait_bounded(b_pv, (npv + t - 1) & 1, abort_flag, a.err_flag))) {
+                    if (!mbar_wait_warp(b_pv, (npv + t - 1) & 1, abort_flag, a.err_flag)) {
                         ok = false;
                         break;
                     }
@@ -617,12 +624,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attn_kernel(const Prefi
                         w[e] = pack_half2(p.x, p.y);
                     }
                     tmem_st16(sb + c / 2, w);
+                    if ((c + 32) % (kPfTile / kPfParts) == 0) {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(b_p + 8 * (c / (kPfTile / kPfParts)));
+                    }
                 }
                 lsum += ((l4[0].x + l4[0].y) + (l4[1].x + l4[1].y)) + ((l4[2].x + l4[2].y) + (l4[3].x + l4[3].y));
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(b_p);
             }
             ns += nt;
             // the next item's Q: this tile's last S = Q K^T has been read, and the MMA
@@ -631,13 +640,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attn_kernel(const Prefi
             PfItem nxt;
             const bool have_next = ok && pf_next(a, ord, total, k, nxt);
             if (have_next) {
-                if (!__all_sync(kPfFull, mbar_wait_bounded(b_qf, ni & 1, abort_flag, a.err_flag))) ok = false;
+                if (!mbar_wait_warp(b_qf, ni & 1, abort_flag, a.err_flag)) ok = false;
                 else load_q(nxt);
             }
             ++ni;
             // ---- epilogue: O / l * v_scale -> fp16 output row (every lane loads, valid rows store) ----
             if (nt > 0 && ok &&
-                __all_sync(kPfFull, !*abort_flag && mbar_wait_bounded(b_pv, (npv + nt - 1) & 1, abort_flag, a.err_flag))) {
+                __all_sync(kPfFull, *abort_flag == 0) && mbar_wait_warp(b_pv, (npv + nt - 1) & 1, abort_flag, a.err_flag)) {
                 tc_fence_after();
                 const float coef = lsum > 0.f ? a.out_scale / lsum : 0.f;
                 __half *orow = static_cast<__half *>(a.out) + ((int64_t)(q0 + (row_ok ? i : 0)) * a.num_q_heads + h) * kPfD;
