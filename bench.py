@@ -55,7 +55,7 @@ GRAPH_STEPS = 10   # steps captured in one CUDA graph
 
 # source files each attention kernel is compiled from (for the profile hash)
 KERNEL_SOURCES = {
-    "prefill_attn_kernel": ["kvq_prefill.cu", "kvq_tcgen05.cuh", "kvq_device.cuh"],
+    "prefill_attn_kernel": ["kvq_prefill.cu", "kvq_tcgen05.cuh", "kvq_warp.cuh", "kvq_device.cuh"],
     "attn_split_kernel": ["kvq_attn_kernel.cuh", "kvq_merge.cuh", "kvq_device.cuh"],
     "attn_tc_kernel": ["kvq_attn_tc.cu", "kvq_attn_kernel.cuh", "kvq_merge.cuh", "kvq_tcgen05.cuh", "kvq_device.cuh"],
 }

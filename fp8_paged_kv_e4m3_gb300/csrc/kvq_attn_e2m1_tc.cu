@@ -37,6 +37,7 @@
 #include "kvq_attn_kernel.cuh"
 #include "kvq_e2m1.cuh"
 #include "kvq_tcgen05.cuh"
+#include "kvq_warp.cuh"
 
 namespace kvq {
 

@@ -107,30 +107,6 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
     }
 }
 
-// The same for a whole warp, all of whose lanes get the same answer.  Every try
-// is followed by a vote, so that the branch is the warp's: with each lane
-// leaving mbar_wait_bounded's loop by itself, a wait for a phase long complete
-// took 200 to 400 cycles in the tcgen05 kernel of the E2M1 cache.
-__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int *abort, int32_t *err_flag)
-{
-    if (__builtin_expect(__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)), 1)) return true;
-    uint64_t t0 = 0;
-#pragma unroll 1
-    for (uint32_t it = 1;; ++it) {
-        if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
-        if ((it & 63u) == 0u) {
-            if (__any_sync(0xFFFFFFFFu, *abort != 0)) return false;
-            const uint64_t now = global_timer_ns();
-            if (t0 == 0) t0 = now;
-            if (__any_sync(0xFFFFFFFFu, now - t0 > kWaitLimitNs)) {
-                *abort = 1;
-                report(err_flag, KVQ_DEV_TIMEOUT);
-                return false;
-            }
-        }
-    }
-}
-
 // ---------------------------------------------------------------------------
 // 1-D bulk TMA: global -> shared, completion counted on an mbarrier.
 // Both addresses 16-byte aligned, size a multiple of 16.

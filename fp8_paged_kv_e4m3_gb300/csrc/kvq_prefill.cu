@@ -54,6 +54,7 @@
 #include "kvq_e2m1.cuh"
 #include "kvq_internal.h"
 #include "kvq_tcgen05.cuh"
+#include "kvq_warp.cuh"
 
 namespace kvq {
 

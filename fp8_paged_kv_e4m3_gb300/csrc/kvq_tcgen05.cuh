@@ -110,14 +110,6 @@ __device__ __forceinline__ void tmem_regs_ready(uint32_t (&r)[16])
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// one lane of a converged warp
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
-
 // named barrier over `count` threads (ids other than 0, which __syncthreads uses)
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t count)
 {
