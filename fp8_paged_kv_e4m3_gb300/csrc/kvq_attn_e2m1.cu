@@ -6,8 +6,9 @@
 
 namespace kvq {
 
-// whether a call runs on the tcgen05 kernel.  At 16 rows the mma.sync kernel is as fast on ragged batches and
-// faster on even ones (32 x 8192: 53 against 59 us); at 32 rows 89 against 76, ragged 210 against 154.
+// whether a call runs on the tcgen05 kernel, which takes the same time for any number of rows up to 32.  Up to 16
+// rows the mma.sync kernel is faster (32 x 8192: 53 us against 68; ragged 108 against 136), beyond them slower
+// (32 rows: 89 us against 68; ragged 210 against 137).
 static bool e2m1_uses_tc(int head_dim, int rows, bool topk) { return head_dim == 128 && rows > 16 && !topk; }
 
 // The numbers of splits worth a look: those that fill k whole waves of `resident` CTAs, and `most`.
@@ -29,7 +30,8 @@ int32_t e2m1_splits(int head_dim, bool topk, int32_t batch, int32_t num_kv_heads
     if (e2m1_uses_tc(head_dim, rows, topk)) {
         // A CTA costs about 8 us beside 2 us per tile of 128 tokens (two CTAs per SM), which for full
         // sequences gives waves * (tiles / splits * 2 + 8); of the numbers within a tenth of the least, the
-        // largest, which balances varied lengths best.
+        // largest, which balances varied lengths best (64 sequences of 1K to 32K: 3, 4, 6 splits 138, 137, 145 us;
+        // 32 x 8192: 2, 4, 6 splits 69, 75, 83 us).
         const int64_t resident = int64_t(device_sm_count()) * (rows <= 32 ? 2 : 1);
         const double tiles = (max_pages + 31) / 32;
         auto cost = [&](int32_t s, int64_t waves) { return double(waves) * (std::ceil(tiles / s) * 2.0 + 8.0); };

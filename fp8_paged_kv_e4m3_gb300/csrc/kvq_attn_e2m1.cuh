@@ -8,9 +8,10 @@
 // M, query rows on N) with binary32 sums and the layer scales hoisted.
 //
 // One CTA of W warps per (split, kv head, sequence); a warp takes units of 32
-// tokens (two tiles of four pages) and keeps its own softmax.  A thread loads
-// from global memory exactly the bytes of its own matrix fragments, so nothing
-// goes through shared memory and no warp waits for another until the merge:
+// tokens (two tiles of four pages) and keeps its own softmax.  Units come
+// through a ring of the warp's own in shared memory, copied ahead by cp.async:
+// a lane copies exactly the bytes of its own matrix fragments and reads them
+// back itself, so no lane and no warp waits for another until the merge:
 //   rows of a K tile   tile row r < 8 is token r % 2 of page r / 2, row r + 8
 //                      its token 2 + r % 2.  Lane (gid, t) holds the D / 4
 //                      channels from t D / 4 on of both rows, and their scales.
@@ -21,6 +22,16 @@
 //                      one conversion gives one channel of both.
 // The order of channels and tokens inside a product is free as long as both
 // operands share it: Q is loaded, and O stored, in this order.
+//
+// What bounds it.  A cached element is 0.5625 bytes, half an E4M3 one, but costs
+// the same conversion, scaling and product, so where the E4M3 kernel waits for
+// memory this one also fills the ALU: a token's K and V (256 channels) take 128
+// conversions and 128 products by block scales, 16 lanes a clock and scheduler
+// each.  8 query rows a kv head, 4 kv heads, head_dim 128: B 4 x 262144 tokens
+// 111 us (5.45 TB/s, 80 % of the copy peak; ALU 50 % and issue slots 58 % busy);
+// B 32 x 32768 116 us (77 %); B 32 x 4096 20.6 us (54 %: one wave, of which the
+// first pages' arrival and the merge take about 5 us).  With 16 rows 53 us at
+// B 32 x 8192 (2.9 TB/s).
 #pragma once
 
 #include <cfloat>
@@ -269,9 +280,11 @@ __device__ __forceinline__ void softmax_unit(const float (&sc)[NT][kUnitTiles][4
 // NT n-tiles of 8 query rows per warp; RW warps share the same tokens and split
 // the query rows, the W / RW groups of warps split the tokens.
 // LISTS: the call has top-k lists (a sequence of it may have none).  LPT: the
-// sequences are taken longest first.  MERGE: the splits of one (sequence, kv head) are one thread-block cluster; after
-// a cluster barrier its CTAs merge the partials (the combine's function, hence
-// its bits) and write the output themselves.
+// sequences are taken longest first.  Both are instances of their own because
+// their code, unused, cost the others registers (ragged batch 94 -> 85 us).
+// MERGE: the splits of one (sequence, kv head) are one thread-block cluster;
+// after a cluster barrier its CTAs merge the partials (the combine's function,
+// hence its bits) and write the output themselves.
 template <int D, int NT, int RW, int W, bool MERGE, bool LISTS, bool LPT>
 __global__ void __launch_bounds__(32 * W, ctas_per_sm<NT, W>()) attn_e2m1_kernel(const AttnArgs a)
 {

@@ -20,12 +20,14 @@
 //    a row's reference moves only when a score rises more than 2^8 above it,
 //    decided by one OR-reduction of a half's four warps a tile; P^T (fp16) to
 //    shared memory; row sums in registers.
-// 64 sequences of 1K to 32K, 4 kv heads, 32 rows, 4 splits: 143 us, 2.4 TB/s of pages, a
-// tile in 1.2 us on an SM's two CTAs (the mma.sync kernel: 210 us).  A tile takes 4800
-// warp instructions, about half of them the conversion to fp16, a third the softmax: 57 % of the
-// issue slots and 43 % of the ALU are in use, the tensor cores 12 %, DRAM 30 %.  What
-// bounds it is a tile's chain (scores, maxima over the warps, P, product, O rescaled)
-// with two CTAs to hide it; 72 registers a thread leave no room for a third.
+// 64 sequences of 1K to 32K, 4 kv heads, 32 rows, 4 splits: 137.5 us, 2.4 TB/s of
+// pages, a tile in 1.1 us on an SM's two CTAs (the mma.sync kernel: 210 us).  A tile
+// takes 4700 warp instructions: 56 % of the issue slots and 44 % of the ALU are busy,
+// the tensor cores 12 %, DRAM 31 %.  What bounds it is the decode warps' chain over a
+// tile (about 2400 cycles alone on an SM, of which the two conversions take 900 and the
+// reads of the raw pages with the next copies' issue 900), and two CTAs per SM to hide
+// it.  Measured and rejected: a bulk copy a page in place of the 16-byte pieces (143 ->
+// 164 us), the copies issued between the blocks of the conversion (143 -> 155 us).
 // Every wait is bounded (about 2 s): on expiry the CTA reports
 // KVQ_DEV_TIMEOUT, lets its copies and MMAs drain, gives its rows zero weight
 // and frees its tensor memory.

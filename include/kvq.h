@@ -459,7 +459,8 @@ int paged_prefill_attn_fp16(const void *q, const void *k_cache, const void *v_ca
  *   KVQ_ROPE_YARN    interpolation by parts (YaRN, Peng et al. 2023): with
  *     d(beta) = rot_dim ln(original_positions / (2 pi beta)) / (2 ln base),
  *     low = max(floor(d(beta_fast)), 0), high = min(ceil(d(beta_slow)),
- *     rot_dim - 1), r_j = (j - low) / (high - low) clamped to [0, 1]:
+ *     rot_dim - 1) (low + 0.001 where that is not above low), r_j =
+ *     (j - low) / (high - low) clamped to [0, 1]:
  *     f_j (1 - r_j) + f_j r_j / factor
  *   table : device float32 [max_positions][rot_dim]; rot_dim a multiple of 16
  *   base > 1; factor >= 1 (LINEAR, YARN); original_positions >= 1 and
@@ -568,7 +569,15 @@ int kv_gather_e2m1(const uint8_t *k_cache, const uint8_t *v_cache, int64_t num_p
  * _partial form with these pools, the same parameters, workspace, masks,
  * top-k lists and errors.  Of the flags only KVQ_ATTN_STRICT_ORDER applies;
  * the others return KVQ_ERR_UNSUPPORTED.  kvq_lse_combine merges the
- * partials.  Two launches: attention, combine. */
+ * partials.  Here a split's m is the reference its sum was taken against,
+ * which may lie below the largest score by up to ln 2^8 (m + ln l is the
+ * log-sum-exp either way).  A row that met a NaN score is handed on as NaN
+ * with m = FLT_MAX, l = 1.  _partial fills every one of p->num_splits splits;
+ * the full call may use fewer than the workspace holds, orders sequences by
+ * length where that pays, and launches the attention and the combine, or one
+ * kernel where the splits merge as a thread-block cluster (up to 8 splits on
+ * a grid resident at once, no top-k list; at head_dim 128 up to 16 query rows
+ * per KV head). */
 int paged_decode_attn_e2m1(const void *q, const uint8_t *k_cache, const uint8_t *v_cache, int64_t num_pages,
                            const int32_t *block_tables, const int32_t *context_lens, float k_scale, float v_scale,
                            const int32_t *topk_idx, const int32_t *topk_lens, float *workspace, size_t workspace_bytes,
