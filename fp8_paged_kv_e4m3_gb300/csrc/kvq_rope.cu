@@ -11,11 +11,11 @@
 // Bound by memory: every element is read once and written once.  8192 tokens,
 // 32 query and 4 kv heads of 128 channels: into E4M3 pages 30.0 us (80 % of the
 // copy peak over the 164 MB moved); 8240 tokens into E2M1 pages, half of the
-// channels rotated, 35.5 us (75 %), where the block maxima and the divisions of
-// a block of 16 channels keep the ALU 41 % busy; 4096 tokens of 8 kv heads
-// appended to E2M1 pages without a rotation 12.7 us (50 %: 43 MB), read back
-// 4.8 us with the rows in L2.  The few tokens of a decode step take 2.3 to
-// 4.0 us, a launch and two dependent reads.
+// channels rotated, and their rows read back 35.5 us (75 %), where the maximum,
+// the quotient and the reciprocal of each block of 16 channels keep the ALU 41 %
+// busy; 4096 tokens of 8 kv heads appended to E2M1 pages without a rotation and
+// read back 12.7 us (43 MB).  The few tokens of a decode step take 2.3 to 4.0 us,
+// a launch and two dependent reads.
 #include <cstdint>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
