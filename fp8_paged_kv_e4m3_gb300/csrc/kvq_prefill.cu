@@ -586,26 +586,26 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attn_kernel(const Prefi
                 // row's sum and (once PV(t-1) is complete) its O row are rescaled.  The
                 // O pass is warp-wide; lanes whose reference stays scale by 1.
                 const bool move = mx > ref + 8.f;
-                const float corr = !move ? 1.f : (ref == -INFINITY ? 0.f : fast_exp2(ref - mx));
-                if (move) {
+                if (__builtin_expect(__any_sync(kPfFull, move), 0)) {
+                    const float corr = !move ? 1.f : (ref == -INFINITY ? 0.f : fast_exp2(ref - mx));
+                    if (move) ref = mx;
                     lsum *= corr;
-                    ref = mx;
-                }
-                if (t > 0 && __any_sync(kPfFull, move)) {
-                    if (!mbar_wait_warp(b_pv, (npv + t - 1) & 1, abort_flag, a.err_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
+                    if (t > 0) {
+                        if (!mbar_wait_warp(b_pv, (npv + t - 1) & 1, abort_flag, a.err_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < kPfD; c += 16) {
-                        uint32_t r16[16];
-                        tmem_ld16(ob + c, r16);
-                        tmem_wait_ld();
-                        tmem_regs_ready(r16);
+                        for (int c = 0; c < kPfD; c += 16) {
+                            uint32_t r16[16];
+                            tmem_ld16(ob + c, r16);
+                            tmem_wait_ld();
+                            tmem_regs_ready(r16);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) r16[e] = __float_as_uint(__uint_as_float(r16[e]) * corr);
-                        tmem_st16(ob + c, r16);
+                            for (int e = 0; e < 16; ++e) r16[e] = __float_as_uint(__uint_as_float(r16[e]) * corr);
+                            tmem_st16(ob + c, r16);
+                        }
                     }
                 }
                 // P = 2^(s qk - ref) as fp16 pairs over the first 64 columns of S; the
