@@ -7,7 +7,7 @@
 namespace kvq {
 
 // whether a call runs on the tcgen05 kernel, which takes the same time for any number of rows up to 32.  Up to 16
-// rows the mma.sync kernel is faster (32 x 8192: 53 us against 68; ragged 108 against 136), beyond them slower
+// rows the mma.sync kernel is faster (32 x 8192: 51 us against 68; ragged 108 against 136), beyond them slower
 // (32 rows: 89 us against 68; ragged 210 against 137).
 static bool e2m1_uses_tc(int head_dim, int rows, bool topk) { return head_dim == 128 && rows > 16 && !topk; }
 
@@ -44,12 +44,15 @@ int32_t e2m1_splits(int head_dim, bool topk, int32_t batch, int32_t num_kv_heads
     }
     if (topk) return most;   // lists and whole contexts side by side: varied work again
     const int64_t resident = e2m1_resident(rows);
-    const int32_t fewest = most / 4 > 8 ? most / 4 : 8;
-    double score = 0.0;
+    auto score = [&](int32_t s, int64_t waves) { return double(pairs * s) / double(waves * resident) / (1.0 + 0.01 * s); };
+    // Up to 8 splits balance a batch of varied lengths by their number, so that fewer (3/5 of them at least) have to
+    // fill their waves better by a quarter.  128 pairs: 16 rows x 8192, 7 instead of 8, 53 -> 51 us (contexts of 410 to
+    // 8192 35 -> 31); 8 rows x 6000, 4 instead of 6, 32 -> 28 us (300 to 6000 16.7 -> 17.5).
+    const int32_t fewest = most > 8 ? (most / 4 > 8 ? most / 4 : 8) : (3 * most + 4) / 5;
+    double least = most > 8 ? 0.0 : 1.25 * score(most, (pairs * most + resident - 1) / resident);
     e2m1_each_filling(pairs, resident, most, [&](int32_t s, int64_t waves) {
-        const double v = double(pairs * s) / double(waves * resident) / (1.0 + 0.01 * s);
-        if (s >= fewest && v > score) {
-            score = v;
+        if (s >= fewest && score(s, waves) > least) {
+            least = score(s, waves);
             best = s;
         }
     });

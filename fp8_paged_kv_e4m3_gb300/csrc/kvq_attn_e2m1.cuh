@@ -30,8 +30,8 @@
 // each.  8 query rows a kv head, 4 kv heads, head_dim 128: B 4 x 262144 tokens
 // 111 us (5.45 TB/s, 80 % of the copy peak; ALU 50 % and issue slots 58 % busy);
 // B 32 x 32768 116 us (77 %); B 32 x 4096 20.6 us (54 %: one wave, of which the
-// first pages' arrival and the merge take about 5 us).  With 16 rows 53 us at
-// B 32 x 8192 (2.9 TB/s).
+// first pages' arrival and the merge take about 5 us).  With 16 rows 51 us at
+// B 32 x 8192 (3.0 TB/s).
 #pragma once
 
 #include <cfloat>

@@ -122,8 +122,8 @@ cudaError_t launch_attention_e2m1_d64(const AttnArgs &a, bool merge, cudaStream_
 cudaError_t launch_attention_e2m1_tc(const AttnArgs &a, cudaStream_t stream);
 // the splits a full E2M1 call uses where the caller leaves the number open and the library's rule gives
 // `most`: never more, since the workspace is sized for those.  On the mma.sync kernel, of 8 (or most / 4) to
-// most, those that fill whole waves of resident CTAs, at about 1 % of the time each for the merge; up to 8
-// stay as they are, since a batch of varied lengths balances by them.
+// most, those that fill whole waves of resident CTAs, at about 1 % of the time each for the merge; where most is
+// 8 or fewer, most itself unless fewer fill the waves much better.
 int32_t e2m1_splits(int head_dim, bool topk, int32_t batch, int32_t num_kv_heads, int rows, int32_t max_pages, int32_t most);
 // append with rotary positions, or (rotate false) the plain append to E2M1 pools; the E2M1
 // read-back; the rotation table (kvq_rope.cu)
