@@ -5,7 +5,7 @@
 Each .cu file under csrc/ compiles in its own nvcc process (in parallel);
 the objects link into fp8_paged_kv_e4m3_gb300/_build/libkvq.so with the
 CUDA runtime linked statically.  No torch headers are involved: the library
-is a plain C ABI.  kvq_pycall.c, the CPython module that marshals some calls,
+is a plain C ABI.  kvq_pycall.cpp, the CPython module that marshals some calls,
 compiles to _build/kvq_pycall.so.
 """
 from __future__ import annotations
@@ -13,6 +13,7 @@ from __future__ import annotations
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -25,7 +26,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libkvq.so")
-PYCALL = os.path.join(BUILD, "kvq_pycall.so")   # CPython module that marshals the calls (kvq_pycall.c)
+PYCALL = os.path.join(BUILD, "kvq_pycall.so")   # CPython module that marshals the calls (kvq_pycall.cpp)
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -44,7 +45,7 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.c")) + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) \
+    return _sources() + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) \
         + glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
@@ -56,16 +57,18 @@ def up_to_date() -> bool:
 
 
 def _build_pycall() -> None:
-    cc = shutil.which("cc") or shutil.which("gcc")
+    cc = shutil.which("c++") or shutil.which("g++")
     if not cc:
-        raise RuntimeError("no C compiler: the call module cannot be built")
+        raise RuntimeError("no C++ compiler: the call module cannot be built")
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
     tmp = PYCALL + f".{os.getpid()}.tmp"
-    cmd = [cc, "-O2", "-std=gnu11", "-shared", "-fPIC", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
-           os.path.join(CSRC, "kvq_pycall.c"), "-o", tmp]
+    cmd = [cc, "-O2", "-std=c++17", "-shared", "-fPIC", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(torch, "include"), "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           os.path.join(CSRC, "kvq_pycall.cpp"), "-o", tmp, "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stderr)
-        raise RuntimeError("cc failed:\n" + " ".join(cmd))
+        raise RuntimeError("c++ failed:\n" + " ".join(cmd))
     os.replace(tmp, PYCALL)
 
 
@@ -83,7 +86,9 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
             objs.append(obj)
             cmd = [cc, *ARCH, *FLAGS, *extra, "-c", src, "-o", obj]
             jobs.append(ex.submit(subprocess.run, cmd, capture_output=True, text=True))
+        pycall = ex.submit(_build_pycall)
         results = [j.result() for j in jobs]
+        pycall.result()
     for r in results:
         if r.returncode != 0 or (ptxas_verbose and r.stderr):
             sys.stderr.write(r.stderr)
@@ -95,7 +100,6 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
     if r.returncode != 0:
         sys.stderr.write(r.stderr)
         raise RuntimeError("link failed")
-    _build_pycall()
     os.replace(tmp, LIB)
     return LIB
 

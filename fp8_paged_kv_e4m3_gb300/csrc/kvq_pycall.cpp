@@ -1,23 +1,25 @@
 /*
- * kvq_pycall.c -- a CPython module that marshals the calls of the 4-bit cache
+ * kvq_pycall.cpp -- a CPython module that marshals the calls of the 4-bit cache
  * and the rotary appends.  It checks the tensors (type, device, shape,
- * layout) and calls the C ABI, as kvq.py does through ctypes, but a call's host
- * time is a few attribute reads in C: on small calls, which are as long as
- * their host time, ctypes marshalling costs more than the kernels.
+ * layout) and calls the C ABI, as kvq.py does through ctypes, but reads the
+ * tensors in C++: on small calls, which are as long as their host time, ctypes
+ * marshalling costs more than the kernels (a decode call 21.6 us).
  *
  * Every function returns the C ABI's status, or None when an argument is not
  * what a plain call passes; kvq.py then takes its own path, whose checks name
- * the argument.  No torch headers: tensors are read through their Python
- * attributes.
+ * the argument.  Of torch only tensors are read (torch.Tensor and Parameter
+ * themselves, no subclass).
  */
 #define PY_SSIZE_T_CLEAN
-#include <Python.h>
+#include <torch/csrc/autograd/python_variable.h>
 #include <stdint.h>
 
 #include "kvq.h"
 
+namespace {
+
 /* the library's entry points and torch's objects, set by setup() */
-static struct {
+struct {
     __typeof__(&paged_decode_attn_e2m1) decode;
     __typeof__(&paged_decode_attn_e2m1_partial) decode_partial;
     __typeof__(&paged_prefill_attn_e2m1) prefill;
@@ -27,18 +29,26 @@ static struct {
     __typeof__(&kv_append_rope_e2m1) rope_e2m1;
     __typeof__(&kv_append_rope_fp16) rope_fp16;
 } fn;
-static PyObject *t_half, *t_float, *t_int, *t_byte, *get_stream, *get_device;
-static PyObject *s_dtype, *s_shape, *s_device, *s_contiguous, *s_pointer, *s_stride;
+PyObject *get_stream, *get_device;
+constexpr at::ScalarType t_half = at::kHalf, t_float = at::kFloat, t_int = at::kInt, t_byte = at::kByte;
 
 #define MAX_DIMS 4
 
-typedef struct {
-    void *p;
-    int64_t dim[MAX_DIMS];
-    int64_t stride;      /* between tokens, where asked for */
-} view;
+/* a pointer of whatever type the C ABI asks for */
+struct address {
+    void *a = nullptr;
+    template <typename T>
+    operator T *() const { return static_cast<T *>(a); }
+    explicit operator bool() const { return a != nullptr; }
+};
 
-static int long_of(PyObject *o, int64_t *x)
+struct view {
+    address p;
+    int64_t dim[MAX_DIMS] = {};
+    int64_t stride = 0;  /* between tokens, where asked for */
+};
+
+int long_of(PyObject *o, int64_t *x)
 {
     if (!o) return 0;
     *x = PyLong_AsLongLong(o);
@@ -48,69 +58,51 @@ static int long_of(PyObject *o, int64_t *x)
 
 /* Reads tensor `o`; `heads`: 3 dims of which the last two are contiguous, any stride between tokens.
  * 0 when it is not of this type, number of dims and layout, or not on device `dev` (*dev = -1: any, kept). */
-static int tensor(PyObject *o, PyObject *dtype, int dims, int heads, int64_t *dev, view *v)
-{
-    int64_t x;
-    PyObject *a = PyObject_GetAttr(o, s_dtype);
-    if (!a) return 0;
-    Py_DECREF(a);                        /* a dtype is a constant of torch's */
-    if (a != dtype) return 0;
-    if (!long_of(PyObject_CallMethodNoArgs(o, s_device), &x) || x < 0) return 0;
+int tensor(PyObject *o, at::ScalarType dtype, int dims, int heads, int64_t *dev, view *v)
+try {
+    if (!THPVariable_CheckExact(o)) return 0;
+    const at::Tensor &t = THPVariable_Unpack(o);
+    if (!t.defined() || t.scalar_type() != dtype || t.layout() != at::kStrided || !t.is_cuda() || t.dim() != dims) return 0;
+    const int64_t x = t.get_device();
     if (*dev < 0) *dev = x;
     if (x != *dev) return 0;
-    a = PyObject_GetAttr(o, s_shape);
-    if (!a) return 0;
-    if (!PyTuple_Check(a) || PyTuple_GET_SIZE(a) != dims) {
-        Py_DECREF(a);
-        return 0;
-    }
-    for (int i = 0; i < dims; ++i) v->dim[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(a, i));
-    Py_DECREF(a);
+    const at::IntArrayRef shape = t.sizes(), st = t.strides();
+    for (int i = 0; i < dims; ++i) v->dim[i] = shape[i];
     if (heads) {
-        a = PyObject_CallMethodNoArgs(o, s_stride);
-        if (!a) return 0;
-        const int tuple = PyTuple_Check(a) && PyTuple_GET_SIZE(a) == 3;
-        int64_t st[3] = {0, 0, 0};
-        for (int i = 0; tuple && i < 3; ++i) st[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(a, i));
-        Py_DECREF(a);
-        if (!tuple || (v->dim[2] > 1 && st[2] != 1) || (v->dim[1] > 1 && st[1] != v->dim[2])) return 0;
+        if ((v->dim[2] > 1 && st[2] != 1) || (v->dim[1] > 1 && st[1] != v->dim[2])) return 0;
         v->stride = v->dim[1] * v->dim[2];
         if (v->dim[0] > 1) {
             if (st[0] < v->stride) return 0;
             v->stride = st[0];
         }
-    } else {
-        a = PyObject_CallMethodNoArgs(o, s_contiguous);
-        if (!a) return 0;
-        Py_DECREF(a);
-        if (a != Py_True) return 0;
+    } else if (!t.is_contiguous()) {
+        return 0;
     }
-    a = PyObject_CallMethodNoArgs(o, s_pointer);
-    if (!a) return 0;
-    v->p = PyLong_AsVoidPtr(a);
-    Py_DECREF(a);
-    return !PyErr_Occurred();
+    v->p.a = t.data_ptr();
+    return 1;
+} catch (...) {   // a tensor without storage of its own: none of these calls'
+    return 0;
 }
 
 /* an optional int32 tensor of any length (the error flag): its pointer, NULL for None */
-static int flag(PyObject *o, int64_t *dev, void **p)
+int flag(PyObject *o, int64_t *dev, address *p)
 {
     view v;
-    *p = NULL;
+    p->a = nullptr;
     if (o == Py_None) return 1;
     if (!tensor(o, t_int, 1, 0, dev, &v) || v.dim[0] < 1) return 0;
     *p = v.p;
     return 1;
 }
 
-static int real(PyObject *o, float *x)
+int real(PyObject *o, float *x)
 {
     const double d = PyFloat_AsDouble(o);
     *x = (float)d;
     return !(d == -1.0 && PyErr_Occurred());
 }
 
-static int whole(PyObject *o, int32_t *x)
+int whole(PyObject *o, int32_t *x)
 {
     const long d = PyLong_AsLong(o);
     *x = (int32_t)d;
@@ -118,7 +110,7 @@ static int whole(PyObject *o, int32_t *x)
 }
 
 /* torch's current stream on `dev`, when that is the current device */
-static int current_stream(int64_t dev, void **stream)
+int current_stream(int64_t dev, void **stream)
 {
     int64_t x;
     if (!long_of(PyObject_CallNoArgs(get_device), &x) || x != dev) return 0;
@@ -132,14 +124,14 @@ static int current_stream(int64_t dev, void **stream)
     return !PyErr_Occurred();
 }
 
-static PyObject *not_plain(void)
+PyObject *not_plain(void)
 {
     PyErr_Clear();
     Py_RETURN_NONE;
 }
 
 /* a K and a V pool of E2M1 pages, or (page4) of [4][head_dim] elements of `dtype` */
-static int pools(PyObject *k, PyObject *v, PyObject *dtype, int page4, int64_t head_dim, int64_t *dev, view *kc, view *vc)
+int pools(PyObject *k, PyObject *v, at::ScalarType dtype, int page4, int64_t head_dim, int64_t *dev, view *kc, view *vc)
 {
     const int dims = page4 ? 4 : 3;
     if (!tensor(k, dtype, dims, 0, dev, kc) || !tensor(v, dtype, dims, 0, dev, vc)) return 0;
@@ -151,13 +143,14 @@ static int pools(PyObject *k, PyObject *v, PyObject *dtype, int page4, int64_t h
 
 /* (q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale, workspace, out or None, topk_idx, topk_lens,
  *  num_splits, sm_scale, err_flag, split_pages, flags); out None: the partials alone */
-static PyObject *py_decode(PyObject *self, PyObject *const *a, Py_ssize_t n)
+PyObject *py_decode(PyObject *self, PyObject *const *a, Py_ssize_t n)
 {
-    view q, kc, vc, bt, cl, ws, out = {0}, idx = {0}, tl = {0};
+    view q, kc, vc, bt, cl, ws, out, idx, tl;
     int64_t dev = -1;
     float ks, vs, sm;
     int32_t splits, pages, flags;
-    void *err, *stream;
+    address err;
+    void *stream;
     (void)self;
     if (n != 16 || !tensor(a[0], t_half, 4, 0, &dev, &q) || !pools(a[1], a[2], t_byte, 0, q.dim[3], &dev, &kc, &vc) ||
         !tensor(a[3], t_int, 2, 0, &dev, &bt) || !tensor(a[4], t_int, 1, 0, &dev, &cl) || !real(a[5], &ks) ||
@@ -191,13 +184,14 @@ static PyObject *py_decode(PyObject *self, PyObject *const *a, Py_ssize_t n)
 }
 
 /* (q, k_cache, v_cache, block_tables, context_lens, q_start, k_scale, v_scale, workspace, out, max_q_len, sm_scale, err_flag) */
-static PyObject *py_prefill(PyObject *self, PyObject *const *a, Py_ssize_t n)
+PyObject *py_prefill(PyObject *self, PyObject *const *a, Py_ssize_t n)
 {
     view q, kc, vc, bt, cl, qs, ws, out;
     int64_t dev = -1;
     float ks, vs, sm;
     int32_t longest;
-    void *err, *stream;
+    address err;
+    void *stream;
     (void)self;
     if (n != 13 || !tensor(a[0], t_half, 3, 0, &dev, &q) || !pools(a[1], a[2], t_byte, 0, q.dim[2], &dev, &kc, &vc) ||
         !tensor(a[3], t_int, 2, 0, &dev, &bt) || !tensor(a[4], t_int, 1, 0, &dev, &cl) ||
@@ -217,12 +211,13 @@ static PyObject *py_prefill(PyObject *self, PyObject *const *a, Py_ssize_t n)
 }
 
 /* (k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scale, err_flag) */
-static PyObject *py_append(PyObject *self, PyObject *const *a, Py_ssize_t n)
+PyObject *py_append(PyObject *self, PyObject *const *a, Py_ssize_t n)
 {
     view k, v, sl, kc, vc;
     int64_t dev = -1;
     float ks, vs;
-    void *err, *stream;
+    address err;
+    void *stream;
     (void)self;
     if (n != 8 || !tensor(a[0], t_half, 3, 0, &dev, &k) || !tensor(a[1], t_half, 3, 0, &dev, &v) ||
         !tensor(a[2], t_int, 1, 0, &dev, &sl) || !pools(a[3], a[4], t_byte, 0, k.dim[2], &dev, &kc, &vc) ||
@@ -236,12 +231,13 @@ static PyObject *py_append(PyObject *self, PyObject *const *a, Py_ssize_t n)
 }
 
 /* (k_cache, v_cache, slots, k_scale, v_scale, k_out, v_out, err_flag) */
-static PyObject *py_gather(PyObject *self, PyObject *const *a, Py_ssize_t n)
+PyObject *py_gather(PyObject *self, PyObject *const *a, Py_ssize_t n)
 {
     view sl, kc, vc, k, v;
     int64_t dev = -1;
     float ks, vs;
-    void *err, *stream;
+    address err;
+    void *stream;
     (void)self;
     if (n != 8 || !tensor(a[5], t_half, 3, 0, &dev, &k) || !tensor(a[6], t_half, 3, 0, &dev, &v) ||
         !pools(a[0], a[1], t_byte, 0, k.dim[2], &dev, &kc, &vc) || !tensor(a[2], t_int, 1, 0, &dev, &sl) ||
@@ -256,13 +252,14 @@ static PyObject *py_gather(PyObject *self, PyObject *const *a, Py_ssize_t n)
 
 /* (kind, q or None, k_new, v_new, positions, table, slot_mapping, q_out or None, k_cache, v_cache, k_scale, v_scale,
  *  flags, err_flag); kind 0 = E4M3, 1 = fp16, 2 = E2M1 */
-static PyObject *py_rope(PyObject *self, PyObject *const *a, Py_ssize_t n)
+PyObject *py_rope(PyObject *self, PyObject *const *a, Py_ssize_t n)
 {
-    view q = {0}, k, v, pos, tb, sl, qo = {0}, kc, vc;
+    view q, k, v, pos, tb, sl, qo, kc, vc;
     int64_t dev = -1;
     int32_t kind, flags;
     float ks, vs;
-    void *err, *stream;
+    address err;
+    void *stream;
     (void)self;
     if (n != 14 || !whole(a[0], &kind) || !tensor(a[2], t_half, 3, 1, &dev, &k) || !tensor(a[3], t_half, 3, 1, &dev, &v) ||
         !tensor(a[4], t_int, 1, 0, &dev, &pos) || !tensor(a[5], t_float, 2, 0, &dev, &tb) ||
@@ -291,15 +288,14 @@ static PyObject *py_rope(PyObject *self, PyObject *const *a, Py_ssize_t n)
     return PyLong_FromLong(st);
 }
 
-/* (addresses of the eight entry points in the order of `fn`, (float16, float32, int32, uint8), current raw stream of a
- *  device, current device) */
-static PyObject *py_setup(PyObject *self, PyObject *args)
+/* (addresses of the eight entry points in the order of `fn`, current raw stream of a device, current device) */
+PyObject *py_setup(PyObject *self, PyObject *args)
 {
-    PyObject *at, *types;
+    PyObject *at;
     (void)self;
-    if (!PyArg_ParseTuple(args, "O!O!OO", &PyTuple_Type, &at, &PyTuple_Type, &types, &get_stream, &get_device)) return NULL;
-    if (PyTuple_GET_SIZE(at) != 8 || PyTuple_GET_SIZE(types) != 4) {
-        PyErr_SetString(PyExc_ValueError, "eight addresses and four types expected");
+    if (!PyArg_ParseTuple(args, "O!OO", &PyTuple_Type, &at, &get_stream, &get_device)) return NULL;
+    if (PyTuple_GET_SIZE(at) != 8) {
+        PyErr_SetString(PyExc_ValueError, "eight addresses expected");
         return NULL;
     }
     void *p[8];
@@ -313,17 +309,12 @@ static PyObject *py_setup(PyObject *self, PyObject *args)
     fn.rope_e4m3 = (__typeof__(fn.rope_e4m3))p[5];
     fn.rope_e2m1 = (__typeof__(fn.rope_e2m1))p[6];
     fn.rope_fp16 = (__typeof__(fn.rope_fp16))p[7];
-    t_half = PyTuple_GET_ITEM(types, 0);
-    t_float = PyTuple_GET_ITEM(types, 1);
-    t_int = PyTuple_GET_ITEM(types, 2);
-    t_byte = PyTuple_GET_ITEM(types, 3);
-    Py_INCREF(types);        /* kept for the life of the process */
-    Py_INCREF(get_stream);
+    Py_INCREF(get_stream);   /* kept for the life of the process */
     Py_INCREF(get_device);
     Py_RETURN_NONE;
 }
 
-static PyMethodDef methods[] = {{"setup", py_setup, METH_VARARGS, NULL},
+PyMethodDef methods[] = {{"setup", py_setup, METH_VARARGS, NULL},
                                 {"decode", (PyCFunction)(void (*)(void))py_decode, METH_FASTCALL, NULL},
                                 {"prefill", (PyCFunction)(void (*)(void))py_prefill, METH_FASTCALL, NULL},
                                 {"append", (PyCFunction)(void (*)(void))py_append, METH_FASTCALL, NULL},
@@ -331,16 +322,8 @@ static PyMethodDef methods[] = {{"setup", py_setup, METH_VARARGS, NULL},
                                 {"rope", (PyCFunction)(void (*)(void))py_rope, METH_FASTCALL, NULL},
                                 {NULL, NULL, 0, NULL}};
 
-static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "kvq_pycall", NULL, -1, methods, NULL, NULL, NULL, NULL};
+struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "kvq_pycall", NULL, -1, methods, NULL, NULL, NULL, NULL};
 
-PyMODINIT_FUNC PyInit_kvq_pycall(void)
-{
-    s_dtype = PyUnicode_InternFromString("dtype");
-    s_shape = PyUnicode_InternFromString("shape");
-    s_device = PyUnicode_InternFromString("get_device");
-    s_contiguous = PyUnicode_InternFromString("is_contiguous");
-    s_pointer = PyUnicode_InternFromString("data_ptr");
-    s_stride = PyUnicode_InternFromString("stride");
-    if (!s_dtype || !s_shape || !s_device || !s_contiguous || !s_pointer || !s_stride) return NULL;
-    return PyModule_Create(&module);
-}
+}  // namespace
+
+PyMODINIT_FUNC PyInit_kvq_pycall(void) { return PyModule_Create(&module); }

@@ -147,7 +147,7 @@ def load(path: Optional[str] = None):
 
 
 def _load_pycall(lib, path: str):
-    """The CPython module that marshals the E2M1 and rotary calls (kvq_pycall.c).  Its functions return a
+    """The CPython module that marshals the E2M1 and rotary calls (kvq_pycall.cpp).  Its functions return a
     status, or None for arguments that are not those of a plain call: the ctypes path then names them."""
     if not os.path.exists(path):
         raise RuntimeError(f"call module not built: {path} is missing (run `python -m fp8_paged_kv_e4m3_gb300.build`)")
@@ -157,7 +157,7 @@ def _load_pycall(lib, path: str):
     entry = ("paged_decode_attn_e2m1", "paged_decode_attn_e2m1_partial", "paged_prefill_attn_e2m1", "kv_append_e2m1",
              "kv_gather_e2m1", "kv_append_rope_e4m3", "kv_append_rope_e2m1", "kv_append_rope_fp16")
     mod.setup(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in entry),
-              (torch.float16, torch.float32, torch.int32, torch.uint8), _raw_stream, torch.cuda.current_device)
+              _raw_stream, getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device))
     return mod
 
 
