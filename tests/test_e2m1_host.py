@@ -173,3 +173,23 @@ def test_python_binding_refuses_cpu_tensors_and_bad_tables():
     with pytest.raises(ValueError):
         kvq.rope_table(10, 64, scaling="cubic", device="cpu")
     assert kvq.e2m1_page_bytes(128) == 288 and kvq.e2m1_page_bytes(64) == 144
+
+
+def test_call_module_leaves_unusual_arguments_to_the_checks():
+    """The module that marshals the calls answers None (its caller then names what is wrong) for anything that is not a
+    strided CUDA tensor of the right type: no exception, nothing read."""
+    kvq.load()
+
+    class Sub(torch.Tensor):
+        pass
+
+    z = torch.zeros(2, 2, 64, dtype=torch.float16)
+    odd = [z, z.to("meta"), z.as_subclass(Sub), torch.nn.Parameter(z), z.to_sparse(), torch.empty(0), None, 3, "x", object()]
+    for x in odd:
+        for y in (z, x):
+            assert kvq._pycall.append(x, y, x, x, y, 1.0, 1.0, None) is None
+            assert kvq._pycall.gather(x, x, x, 1.0, 1.0, y, y, None) is None
+            assert kvq._pycall.rope(2, x, y, y, x, x, x, y, x, x, 1.0, 1.0, 0, None) is None
+            assert kvq._pycall.prefill(x, y, y, x, x, x, 1.0, 1.0, x, y, 1, 0.0, None) is None
+            assert kvq._pycall.decode(x, y, y, x, x, 1.0, 1.0, x, None, None, None, 0, 0.0, None, 0, 0) is None
+    assert kvq._pycall.append(z, z) is None
