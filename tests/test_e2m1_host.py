@@ -5,6 +5,7 @@ import math
 
 import numpy as np
 import pytest
+import torch
 
 from fp8_paged_kv_e4m3_gb300 import build, kvq
 from tests import _e2m1 as E
